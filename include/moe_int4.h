@@ -378,6 +378,114 @@ int32_t moe_layer_kernel_launches(const moe_cfg_t* cfg, int32_t T);
 #define MOE_PATH_LARGE_STREAMING 3 /* large router, weight-streaming experts */
 int32_t moe_layer_path(const moe_cfg_t* cfg, int32_t T);
 
+/* ---------------------------------------------------------------------------
+ * Int4 weights with group scales: dense projections, and a whole layer for a
+ * few tokens.
+ *
+ * The codes are packed as above (row-major, one row per output feature, two
+ * 4-bit two's-complement codes a byte, element 2j in the low nibble).  A row
+ * of n codes has one scale for every `group` consecutive columns: G =
+ * ceil(n / group) scales, stored row-major [rows][G] (the last group may be
+ * short); weight[r][k] = c[r][k] * scale[r][k / group].  group is a power of
+ * two from 32 to 32768, or 0 for one scale a row ([rows], the format of
+ * moe_layer_forward).  The scales are f32, bf16 or f16 (any finite value,
+ * negative and zero ones included).
+ *
+ * Arithmetic of both operators: f32 sums throughout (except as noted at each
+ * entry point), one rounding to bf16 at the end (none under MOE_OUT_F32).
+ * ------------------------------------------------------------------------- */
+#define MOE_SCALE_F32 0
+#define MOE_SCALE_BF16 1
+#define MOE_SCALE_F16 2
+
+/* A dense projection  out[t][n] = sum_k x[t][k] weight[n][k]  (+ add[t][n]).
+ *   struct_size : sizeof(moe_linear_cfg_t)
+ *   N           : output features (rows of w), 1..2^20
+ *   K           : input features, a multiple of 32, 32..32768
+ *   group       : columns per scale (see above)
+ *   scale_type  : MOE_SCALE_*
+ *   flags       : MOE_OUT_F32 (out is f32), or 0
+ *   ldx         : elements between rows of x (0: K); a multiple of 8, >= K
+ *   ldo, lda    : elements between rows of out and of add (0: N), >= N */
+typedef struct moe_linear_cfg {
+    uint32_t struct_size;
+    int32_t N, K;
+    int32_t group;
+    int32_t scale_type;
+    uint32_t flags;
+    int64_t ldx, ldo, lda;
+} moe_linear_cfg_t;
+
+/* x: bf16 [T][ldx]; w: uint8 [N][K/2]; scales: [N][G]; add: bf16 [T][lda] or
+ * NULL; out: bf16 [T][ldo] (f32 under MOE_OUT_F32); T: 0..2^20.  x, w and
+ * scales are 16-byte aligned, out and add to their element.  The columns of
+ * out's rows past N are left as they are.  out must not overlap x, w or
+ * scales, and may overlap add only as the same bf16 tensor (same pointer and
+ * stride: an in-place update).  No workspace; any number of calls may run at
+ * once. */
+int moe_linear_forward(const void* x, const uint8_t* w, const void* scales, const void* add, void* out, int32_t T,
+                       const moe_linear_cfg_t* cfg, void* stream);
+
+/* Kernels one moe_linear_forward call launches (0: T = 0, or a cfg that the
+ * call would reject). */
+int32_t moe_linear_kernel_launches(const moe_linear_cfg_t* cfg, int32_t T);
+
+/* One MoE layer (router, routed experts, shared expert, combine: the formulas
+ * at the top) for a few tokens, as in decode and in verifying a few
+ * speculated tokens.
+ *   struct_size, H, E, K, I, Is, routed_scaling, topp, topk_idx_out,
+ *   topk_w_out, workspace : as in moe_cfg_t
+ *   group, scale_type     : of all four weight matrices (see above)
+ *   flags                 : MOE_ADD_RESIDUAL, MOE_OUT_F32, MOE_DEBUG_POISON
+ *   workspace_bytes       : at least moe_few_workspace_bytes(cfg, T) */
+typedef struct moe_few_cfg {
+    uint32_t struct_size;
+    int32_t H, E, K, I, Is;
+    float routed_scaling;
+    float topp;
+    int32_t group;
+    int32_t scale_type;
+    uint32_t flags;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t* topk_idx_out;
+    float* topk_w_out;
+} moe_few_cfg_t;
+
+/*   router_w [E][H] f32, router_bias [E] f32, w13 [E][2I][H/2] with s13
+ *   [E][2I][G], w2 [E][H][I/2] with s2 [E][H][G]; shared expert (Is > 0):
+ *   sh_w13 [2Is][H/2], sh_s13 [2Is][G], sh_w2 [H][Is/2], sh_s2 [H][G]; each
+ *   G counted over that matrix's columns, no G dimension with group = 0 */
+typedef struct moe_few_weights {
+    const float* router_w;
+    const float* router_bias;
+    const uint8_t* w13;
+    const void* s13;
+    const uint8_t* w2;
+    const void* s2;
+    const uint8_t* sh_w13;
+    const void* sh_s13;
+    const uint8_t* sh_w2;
+    const void* sh_s2;
+} moe_few_weights_t;
+
+/* Bytes of workspace of a call for T tokens, or of any smaller one (0: a cfg
+ * or T that the call would reject). */
+size_t moe_few_workspace_bytes(const moe_few_cfg_t* cfg, int32_t T);
+
+/* Tokens that one pass of the kernels serves (0: an invalid cfg). */
+int32_t moe_few_pass_tokens(const moe_few_cfg_t* cfg);
+
+/* Kernels one moe_few_forward call launches (0: T = 0, or rejected). */
+int32_t moe_few_kernel_launches(const moe_few_cfg_t* cfg, int32_t T);
+
+/* x: bf16 [T][H]; out: bf16 [T][H] (f32 under MOE_OUT_F32), not overlapping x;
+ * T: 0..2^20.  More than moe_few_pass_tokens(cfg) tokens run in passes of that
+ * many, each reading its experts' weights again: any T is served, and a call
+ * for many tokens belongs to moe_layer_forward (per-row scales). */
+int moe_few_forward(const void* x, const moe_few_weights_t* w, void* out, int32_t T, const moe_few_cfg_t* cfg,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,6 +26,9 @@ __all__ = [
     "MOE_PATH_FUSED_STACK", "MOE_PATH_PER_LAYER",
     "workspace_bytes", "workspace_bytes_upto", "layer_forward", "MoELayer", "decode_max_tokens", "kernel_launches", "layer_path",
     "MOE_PATH_SMALL_BATCH", "MOE_PATH_TENSOR_CORE", "MOE_PATH_LARGE_STREAMING", "LIB_PATH",
+    "moe_linear_cfg_t", "moe_few_cfg_t", "moe_few_weights_t", "MOE_SCALE_F32", "MOE_SCALE_BF16", "MOE_SCALE_F16",
+    "linear_forward", "linear_kernel_launches", "Int4Linear",
+    "few_forward", "few_workspace_bytes", "few_pass_tokens", "few_kernel_launches", "MoEFewLayer",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_int4.so")
@@ -63,6 +66,9 @@ MOE_PATH_LARGE_STREAMING = 3
 MOE_PATH_FUSED_STACK = 4
 MOE_PATH_PER_LAYER = 5
 
+# scale types of the group-scaled int4 operators
+MOE_SCALE_F32, MOE_SCALE_BF16, MOE_SCALE_F16 = range(3)
+
 MOE_STAGE_ROUTE, MOE_STAGE_GATE_UP, MOE_STAGE_DOWN, MOE_STAGE_COMBINE = range(4)
 MOE_NUM_STAGES = 4
 STAGE_NAMES = ("route", "gate_up", "down", "combine")
@@ -71,7 +77,9 @@ STAGE_NAMES = ("route", "gate_up", "down", "combine")
 EXPORTED_SYMBOLS = ("moe_layer_workspace_bytes", "moe_layer_forward", "moe_status_str",
                     "moe_abi_version", "moe_decode_max_tokens", "moe_layer_forward_static_ws",
                     "moe_layer_kernel_launches", "moe_layer_path", "moe_layer_workspace_bytes_upto",
-                    "moe_stack_workspace_bytes", "moe_stack_path", "moe_stack_forward", "moe_stack_trace_offset")
+                    "moe_stack_workspace_bytes", "moe_stack_path", "moe_stack_forward", "moe_stack_trace_offset",
+                    "moe_linear_forward", "moe_linear_kernel_launches", "moe_few_workspace_bytes",
+                    "moe_few_pass_tokens", "moe_few_kernel_launches", "moe_few_forward")
 
 # Scratch capacity of moe_layer_forward_static_ws (the entry point for callers
 # that cannot allocate device memory).
@@ -103,6 +111,26 @@ class moe_stack_weights_t(ctypes.Structure):
                 ("w13", ctypes.c_void_p), ("s13", ctypes.c_void_p),
                 ("w2", ctypes.c_void_p), ("s2", ctypes.c_void_p),
                 ("shared", moe_shared_weights_t)]
+
+
+class moe_linear_cfg_t(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("scale_type", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64), ("lda", ctypes.c_int64)]
+
+
+class moe_few_cfg_t(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("H", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("I", ctypes.c_int32), ("Is", ctypes.c_int32),
+                ("routed_scaling", ctypes.c_float), ("topp", ctypes.c_float), ("group", ctypes.c_int32),
+                ("scale_type", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("topk_idx_out", ctypes.c_void_p), ("topk_w_out", ctypes.c_void_p)]
+
+
+class moe_few_weights_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("router_w", "router_bias", "w13", "s13", "w2", "s2",
+                                               "sh_w13", "sh_s13", "sh_w2", "sh_s2")]
 
 
 def _load() -> ctypes.CDLL:
@@ -138,6 +166,19 @@ def _load() -> ctypes.CDLL:
     L.moe_stack_forward.restype = ctypes.c_int
     L.moe_stack_trace_offset.argtypes = [ctypes.POINTER(moe_cfg_t), ctypes.c_int32, ctypes.c_int32]
     L.moe_stack_trace_offset.restype = ctypes.c_size_t
+    lin, few = ctypes.POINTER(moe_linear_cfg_t), ctypes.POINTER(moe_few_cfg_t)
+    L.moe_linear_forward.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int32, lin, vp]
+    L.moe_linear_forward.restype = ctypes.c_int
+    L.moe_linear_kernel_launches.argtypes = [lin, ctypes.c_int32]
+    L.moe_linear_kernel_launches.restype = ctypes.c_int32
+    L.moe_few_workspace_bytes.argtypes = [few, ctypes.c_int32]
+    L.moe_few_workspace_bytes.restype = ctypes.c_size_t
+    L.moe_few_pass_tokens.argtypes = [few]
+    L.moe_few_pass_tokens.restype = ctypes.c_int32
+    L.moe_few_kernel_launches.argtypes = [few, ctypes.c_int32]
+    L.moe_few_kernel_launches.restype = ctypes.c_int32
+    L.moe_few_forward.argtypes = [vp, ctypes.POINTER(moe_few_weights_t), vp, ctypes.c_int32, few, vp]
+    L.moe_few_forward.restype = ctypes.c_int
     if L.moe_abi_version() != 2:
         raise ImportError("libmoe_int4.so ABI version mismatch")
     return L
@@ -396,3 +437,208 @@ class MoELayer:
         f = flags | self.weight_flags | (MOE_ADD_RESIDUAL if residual else 0)
         return layer_forward(x, self.layer, self.shape, out=out, workspace=self.workspace, flags=f,
                              topk_idx=topk_idx, topk_w=topk_w, stage_events=stage_events)
+
+
+# ---------------------------------------------------------------------------
+# Int4 weights with group scales (include/moe_int4.h)
+# ---------------------------------------------------------------------------
+_SCALE_TYPES = {torch.float32: MOE_SCALE_F32, torch.bfloat16: MOE_SCALE_BF16, torch.float16: MOE_SCALE_F16}
+
+
+def _scale_type(name: str, scales: torch.Tensor) -> int:
+    if scales.dtype not in _SCALE_TYPES:
+        raise ValueError(f"{name}: expected float32, bfloat16 or float16 scales, got {scales.dtype}")
+    return _SCALE_TYPES[scales.dtype]
+
+
+def _scale_shape(rows, cols: int, group: int) -> tuple:
+    """Shape of the scales of a matrix [*rows, cols]: [*rows, ceil(cols / group)], or [*rows] for group 0."""
+    return (*rows, -(-cols // group)) if group else tuple(rows)
+
+
+def _raw_stream(device: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        return stream.cuda_stream
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _rows_of(name: str, t: torch.Tensor, dtypes, shape, device) -> int:
+    """The elements between rows of a 2-D tensor whose rows are contiguous (any distance for one row)."""
+    if not t.is_cuda or t.device != device or t.dtype not in dtypes or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected a {' or '.join(map(str, dtypes))} tensor of shape {shape} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: expected contiguous rows, got strides {t.stride()}")
+    if shape[0] > 1:
+        if t.stride(0) < shape[1]:
+            raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+        return t.stride(0)
+    return 0
+
+
+class Int4Linear:
+    """A dense projection with int4 weights and group scales (``moe_linear_forward``).
+
+    ``w``: uint8 [N, K/2] packed codes; ``scales``: float32, bfloat16 or float16 [N, ceil(K/group)]
+    ([N] with ``group`` = 0, one scale a row).  Calls may run at the same time, on any stream of the
+    weights' device."""
+
+    def __init__(self, w: torch.Tensor, scales: torch.Tensor, group: int = 128):
+        if w.dim() != 2:
+            raise ValueError(f"w: expected [N, K/2] codes, got shape {tuple(w.shape)}")
+        self.N, self.K, self.group = w.shape[0], 2 * w.shape[1], int(group)
+        if self.group < 0:
+            raise ValueError(f"group: {group}")
+        _check_dev("w", w, torch.uint8)
+        _check_dev("scales", scales, scales.dtype, _scale_shape((self.N,), self.K, self.group))
+        if scales.device != w.device:
+            raise ValueError(f"w is on {w.device}, scales on {scales.device}")
+        self.w, self.scales, self.device = w, scales, w.device
+        self.cfg = moe_linear_cfg_t(struct_size=ctypes.sizeof(moe_linear_cfg_t), N=self.N, K=self.K, group=self.group,
+                                    scale_type=_scale_type("scales", scales))
+        if lib.moe_linear_kernel_launches(ctypes.byref(self.cfg), 1) == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED, "moe_linear_forward")
+
+    def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                 flags: int = 0, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """out[t] = W x[t] (+ add[t]).  x: bfloat16 [T, K], add: bfloat16 [T, N], out: bfloat16 (float32 under
+        MOE_OUT_F32) [T, N]; each may have rows further apart than their length.  ``out`` may be ``add``."""
+        T = x.shape[0]
+        c = moe_linear_cfg_t.from_buffer_copy(self.cfg)
+        c.flags = flags
+        odt = torch.float32 if flags & MOE_OUT_F32 else torch.bfloat16
+        c.ldx = _rows_of("x", x, (torch.bfloat16,), (T, self.K), self.device)
+        if out is None:
+            out = torch.empty((T, self.N), dtype=odt, device=self.device)
+        else:
+            c.ldo = _rows_of("out", out, (odt,), (T, self.N), self.device)
+        ap = None
+        if add is not None:
+            c.lda = _rows_of("add", add, (torch.bfloat16,), (T, self.N), self.device)
+            ap = add.data_ptr()
+        if T == 0:
+            return out
+        with torch.cuda.device(self.device):
+            st = lib.moe_linear_forward(x.data_ptr(), self.w.data_ptr(), self.scales.data_ptr(), ap, out.data_ptr(),
+                                        T, ctypes.byref(c), _raw_stream(self.device, stream))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_linear_forward")
+        return out
+
+
+def linear_forward(x: torch.Tensor, w: torch.Tensor, scales: torch.Tensor, group: int = 128,
+                   out: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None, flags: int = 0,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One call of ``Int4Linear(w, scales, group)``."""
+    return Int4Linear(w, scales, group)(x, out=out, add=add, flags=flags, stream=stream)
+
+
+def linear_kernel_launches(N: int, K: int, T: int, group: int = 128, scale_type: int = MOE_SCALE_F32) -> int:
+    """Kernels one linear call launches for T tokens (0: T = 0, or an unsupported shape)."""
+    c = moe_linear_cfg_t(struct_size=ctypes.sizeof(moe_linear_cfg_t), N=N, K=K, group=group, scale_type=scale_type)
+    return int(lib.moe_linear_kernel_launches(ctypes.byref(c), int(T)))
+
+
+def make_few_cfg(shape, group: int, scale_type: int = MOE_SCALE_F32, flags: int = 0, topp: float = 0.0) -> moe_few_cfg_t:
+    return moe_few_cfg_t(struct_size=ctypes.sizeof(moe_few_cfg_t), H=shape.H, E=shape.E, K=shape.K, I=shape.I,
+                         Is=shape.Is, routed_scaling=float(shape.routed_scaling), topp=float(topp), group=int(group),
+                         scale_type=int(scale_type), flags=int(flags))
+
+
+def few_workspace_bytes(shape, T: int, group: int = 0) -> int:
+    """Workspace of a few-token layer call for up to T tokens (0: an unsupported shape)."""
+    return int(lib.moe_few_workspace_bytes(ctypes.byref(make_few_cfg(shape, group)), int(T)))
+
+
+def few_pass_tokens(shape, group: int = 0) -> int:
+    """Tokens that one pass of the few-token layer's kernels serves (0: an unsupported shape)."""
+    return int(lib.moe_few_pass_tokens(ctypes.byref(make_few_cfg(shape, group))))
+
+
+def few_kernel_launches(shape, T: int, group: int = 0) -> int:
+    """Kernels one few-token layer call launches for T tokens (0: T = 0, or an unsupported shape)."""
+    return int(lib.moe_few_kernel_launches(ctypes.byref(make_few_cfg(shape, group)), int(T)))
+
+
+class MoEFewLayer:
+    """A whole MoE layer for a few tokens (``moe_few_forward``) with group-scaled int4 weights.
+
+    ``layer``: router_w, router_bias, w13, s13, w2, s2 and, when shape.Is > 0, sh_w13, sh_s13, sh_w2, sh_s2, as in
+    ``layer_forward`` but with scales [..., rows, ceil(cols/group)] of one type (float32, bfloat16 or float16);
+    ``group`` = 0 takes ``layer_forward``'s own scales [..., rows].  Holds a workspace for calls of up to
+    ``max_tokens`` tokens: its calls are ordered on one stream; give each stream that may run at the same time (each
+    captured graph among them) a ``workspace`` of its own (``new_workspace``)."""
+
+    def __init__(self, layer: dict, shape, group: int = 0, max_tokens: int = 8, topp: float = 0.0):
+        H, E, I, Is = shape.H, shape.E, shape.I, shape.Is
+        self.layer, self.shape, self.group, self.max_tokens = layer, shape, int(group), int(max_tokens)
+        self.device = layer["w13"].device
+        sdt = layer["s13"].dtype
+        mats = [("w13", (E, 2 * I), H), ("w2", (E, H), I)]
+        if Is > 0:
+            mats += [("sh_w13", (2 * Is,), H), ("sh_w2", (H,), Is)]
+        self.cfg = make_few_cfg(shape, self.group, _scale_type("s13", layer["s13"]), topp=topp)
+        n = int(lib.moe_few_workspace_bytes(ctypes.byref(self.cfg), self.max_tokens))
+        if n == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED, "moe_few_workspace_bytes")
+        _check_dev("router_w", layer["router_w"], torch.float32, (E, H))
+        _check_dev("router_bias", layer["router_bias"], torch.float32, (E,))
+        keys = ["router_w", "router_bias"]
+        for name, rows, cols in mats:
+            sname = name.replace("w", "s")
+            _check_dev(name, layer[name], torch.uint8, (*rows, cols // 2))
+            _check_dev(sname, layer[sname], sdt, _scale_shape(rows, cols, self.group))
+            keys += [name, sname]
+        if any(layer[k].device != self.device for k in keys):
+            raise ValueError(f"the layer's tensors are not all on {self.device}")
+        self.weights = moe_few_weights_t(**{k: layer[k].data_ptr() for k in keys})
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def new_workspace(self) -> torch.Tensor:
+        return torch.empty_like(self.workspace)
+
+    def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, residual: bool = False, flags: int = 0,
+                 topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """The layer's output for x (bfloat16 [T, H]); bfloat16 [T, H], float32 under MOE_OUT_F32."""
+        T, shape = x.shape[0], self.shape
+        if T > self.max_tokens:
+            raise ValueError(f"T={T} exceeds max_tokens={self.max_tokens}")
+        f = flags | (MOE_ADD_RESIDUAL if residual else 0)
+        odt = torch.float32 if f & MOE_OUT_F32 else torch.bfloat16
+        if out is None:
+            out = torch.empty((T, shape.H), dtype=odt, device=self.device)
+        ws = self.workspace if workspace is None else workspace
+        for name, t, dt, sh in (("x", x, torch.bfloat16, (T, shape.H)), ("out", out, odt, (T, shape.H)),
+                                ("topk_idx", topk_idx, torch.int32, (T, shape.K)),
+                                ("topk_w", topk_w, torch.float32, (T, shape.K)), ("workspace", ws, torch.uint8, None)):
+            if t is None:
+                continue
+            _check_dev(name, t, dt, sh)
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the layer on {self.device}")
+        if T == 0:
+            return out
+        c = moe_few_cfg_t.from_buffer_copy(self.cfg)
+        c.flags = f
+        c.workspace, c.workspace_bytes = ws.data_ptr(), ws.numel()
+        c.topk_idx_out = None if topk_idx is None else topk_idx.data_ptr()
+        c.topk_w_out = None if topk_w is None else topk_w.data_ptr()
+        with torch.cuda.device(self.device):
+            st = lib.moe_few_forward(x.data_ptr(), ctypes.byref(self.weights), out.data_ptr(), T, ctypes.byref(c),
+                                     _raw_stream(self.device, stream))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_few_forward")
+        return out
+
+
+def few_forward(x: torch.Tensor, layer: dict, shape, group: int = 0, out: Optional[torch.Tensor] = None,
+                flags: int = 0, topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None, topp: float = 0.0) -> torch.Tensor:
+    """One call of ``MoEFewLayer``, with a workspace of its own."""
+    m = MoEFewLayer(layer, shape, group, max_tokens=max(1, x.shape[0]), topp=topp)
+    if stream is not None:
+        m.workspace.record_stream(stream)  # freed when this call returns: not before the stream is through with it
+    return m(x, out=out, flags=flags, topk_idx=topk_idx, topk_w=topk_w, stream=stream)

@@ -1,0 +1,66 @@
+// Operators on int4 weights with group scales (internal): the arguments of
+// their kernels and the host-side launch entry points.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "moe_common.cuh"
+
+namespace moe {
+
+// Scale types (the MOE_SCALE_* values of the C ABI).
+constexpr int kScaleF32 = 0, kScaleBf16 = 1, kScaleF16 = 2;
+
+// log2 of the columns per scale; kRowGroup: one scale a row (k >> kRowGroup
+// is 0 for every column).
+constexpr int kRowGroup = 31;
+
+struct LinearArgs {
+    const __nv_bfloat16* x;
+    const uint8_t* w;
+    const void* scales;
+    const __nv_bfloat16* add;  // or null
+    void* out;
+    int T, N, K;
+    int gshift, G;  // columns per scale: 1 << gshift; scales per row
+    int stype, out_f32;
+    long long ldx, ldo, lda;
+};
+
+struct FewArgs {
+    const __nv_bfloat16* x;
+    const float* rw;
+    const float* rb;
+    const uint8_t *w13, *w2, *sh_w13, *sh_w2;
+    const void *s13, *s2, *sh_s13, *sh_s2;
+    void* out;
+    int32_t* topk_idx_out;
+    float* topk_w_out;
+    int T, H, E, K, I, Is;
+    float scale, topp;
+    unsigned flags;
+    int gshift, stype;
+    int G13, G2, Gs2;  // scales per row of w13 (and sh_w13), w2, sh_w2
+    // workspace
+    int32_t* idx;  // [T][K]
+    float* wts;    // [T][K]
+    float* h;      // [T*K][I] then [T][Is]: the SwiGLU intermediate
+};
+
+// One scale, as f32.
+__device__ __forceinline__ float load_scale(const void* s, size_t i, int stype) {
+    if (stype == kScaleF32) return __ldg(static_cast<const float*>(s) + i);
+    const unsigned short b = __ldg(static_cast<const unsigned short*>(s) + i);
+    return stype == kScaleBf16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+}
+
+int linear_launches(const LinearArgs& a);
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
+
+int few_pass_tokens(const FewArgs& a);
+int few_pass_launches(const FewArgs& a);
+// Points a's workspace fields into ws (null: only measures); returns the bytes.
+size_t few_workspace(FewArgs& a, void* ws);
+cudaError_t launch_few(const FewArgs& a, cudaStream_t stream);
+
+}  // namespace moe

@@ -1,0 +1,202 @@
+"""moe_linear_forward on the GPU against the 64-bit product."""
+import pytest
+import torch
+
+from tests._group_int4 import codes, gen, linear64, linear_bound, scales
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import int4_expert_ffn_sigmoid_b200 as m
+    return m
+
+
+def check(out, x, w, s, group, add=None):
+    want, b = linear64(x, w, s, group, add), linear_bound(x, w, s, group, add)
+    if out.dtype == torch.bfloat16:  # one rounding: half a step, 2^-8 of the value
+        b = b + 2.0 ** -8 * (want.abs() + b)
+    off = (out.double() - want).abs()
+    assert bool((off <= b + 1e-37).all()), float((off / (b + 1e-37)).max())
+
+
+def make(T, N, K, group, stype, seed, add, dev):
+    g = gen(seed, dev)
+    x = torch.randn((T, K), generator=g, device=dev).to(torch.bfloat16)
+    w, s = codes(g, N, K // 2), scales(g, (N,), K, group, stype)
+    a = torch.randn((T, N), generator=g, device=dev).to(torch.bfloat16) if add else None
+    return x, w, s, a
+
+
+CASES = [
+    # T, N, K, group, scales
+    (1, 1, 32, 32, "f32"), (1, 1, 32, 0, "f32"), (1, 16, 64, 64, "bf16"), (2, 17, 96, 64, "f16"),
+    (3, 7, 256, 32, "f32"), (4, 100, 288, 32, "bf16"), (5, 129, 512, 128, "f16"), (6, 40, 544, 256, "f32"),
+    (7, 1000, 1120, 64, "bf16"), (8, 513, 1024, 32, "f32"), (8, 16, 8192, 512, "f16"), (1, 5001, 1120, 64, "f16"),
+    (1, 2048, 2048, 0, "f32"), (2, 333, 4096, 1024, "bf16"), (1, 3, 32768, 128, "f32"), (8, 48, 32768, 32768, "f32"),
+    (1, 1024, 1024, 128, "bf16"), (4, 6144, 2048, 32, "f32"), (3, 10240, 256, 32, "bf16"), (5, 31, 32, 128, "f32"),
+    (9, 64, 128, 32, "f32"), (10, 1, 96, 32, "f16"), (16, 640, 2048, 128, "bf16"), (17, 129, 160, 64, "f32"),
+    (31, 255, 1120, 64, "f16"), (33, 1000, 992, 32, "f32"), (64, 1024, 1024, 0, "f32"), (64, 130, 6144, 128, "bf16"),
+    (65, 384, 736, 256, "f16"), (100, 77, 4096, 32, "f32"), (128, 512, 512, 64, "bf16"), (130, 257, 2048, 128, "f32"),
+    (257, 200, 320, 32, "bf16"), (300, 1024, 1024, 128, "f16"), (513, 300, 96, 0, "f32"), (1025, 129, 256, 32, "f32"),
+]
+
+
+@pytest.mark.parametrize("T,N,K,group,stype", CASES)
+def test_matches_product(moe, cuda_device, T, N, K, group, stype):
+    x, w, s, a = make(T, N, K, group, stype, T * 131 + N * 7 + K, N % 2 == 0, cuda_device)
+    lin = moe.Int4Linear(w, s, group)
+    out32 = lin(x, add=a, flags=moe.MOE_OUT_F32)
+    out = lin(x, add=a)
+    check(out32, x, w, s, group, a)
+    check(out, x, w, s, group, a)
+    # the bf16 result is the f32 one, rounded once
+    assert torch.equal(out, out32.to(torch.bfloat16))
+    # and the same call gives the same bits
+    assert torch.equal(out32, lin(x, add=a, flags=moe.MOE_OUT_F32))
+    if N * T >= 4096:  # errors of single weights and activations do not add up: 2^-12 covers their r.m.s.
+        want = linear64(x, w, s, group, a)
+        assert float((out32.double() - want).norm() / want.norm()) <= 2.0 ** -12
+
+
+@pytest.mark.parametrize("T", [1, 4, 8, 20, 150])
+def test_strided_rows(moe, cuda_device, T):
+    N, K, group = 200, 416, 32
+    x, w, s, a = make(T, N, K, group, "bf16", 5, True, cuda_device)
+    xs = torch.full((T, K + 24), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+    xs[:, 16:16 + K] = x
+    wide = torch.full((T, 3 * N + 1), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    base = wide.clone()
+    aw = torch.full((T, N + 5), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+    aw[:, 3:3 + N] = a
+    lin = moe.Int4Linear(w, s, group)
+    got = lin(xs[:, 16:16 + K], out=wide[:, N + 1:2 * N + 1], add=aw[:, 3:3 + N])
+    check(got, x, w, s, group, a)
+    base[:, N + 1:2 * N + 1] = got
+    assert torch.equal(wide, base)  # nothing beside the columns was written
+    # in place: the running sum is also the output
+    run = a.clone()
+    lin(x, out=run, add=run)
+    assert torch.equal(run, got)
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_guard_rows(moe, cuda_device, T):
+    """Rows behind the last token and bytes before the first are left as they were."""
+    N, K = 77, 160
+    x, w, s, _ = make(T, N, K, 32, "f32", 9, False, cuda_device)
+    big = torch.full((T + 4, N), 3.0, dtype=torch.bfloat16, device=cuda_device)
+    moe.linear_forward(x, w, s, 32, out=big[2:2 + T])
+    assert bool((big[:2] == 3).all()) and bool((big[2 + T:] == 3).all())
+    check(big[2:2 + T], x, w, s, 32)
+
+
+@pytest.mark.parametrize("T", [1, 8, 24])
+def test_values(moe, cuda_device, T):
+    """Zero, negative, tiny and large scales (one range a row); rows of zeros; activations of very different sizes."""
+    N, K, group = 96, 512, 64
+    x, w, s, _ = make(T, N, K, group, "f32", 21, False, cuda_device)
+    s[0::6] = 0
+    s[1::6] *= -1
+    s[2::6] *= 1e-18
+    s[3::6] *= 1e15
+    w[4::6] = 0x88  # every code -8
+    x[:, 7] *= 3000  # an outlier column
+    x[0, 256:] = 0
+    if T > 1:
+        x[1] *= 1e-20
+        x[2] *= 2.0 ** 60
+        x[3] = 0
+    out = moe.linear_forward(x, w, s, group, flags=moe.MOE_OUT_F32)
+    check(out, x, w, s, group)
+    assert bool((out[:, 0::6] == 0).all())
+    if T > 1:
+        assert bool((out[3] == 0).all())
+
+
+@pytest.mark.parametrize("T", [2, 8, 30, 140])
+def test_non_finite_rows(moe, cuda_device, T):
+    """A token that holds NaN or an infinity gives no number anywhere; the others are untouched."""
+    N, K, group = 130, 512, 32
+    x, w, s, _ = make(T, N, K, group, "bf16", 33, False, cuda_device)
+    lin = moe.Int4Linear(w, s, group)
+    clean = lin(x)
+    bad = x.clone()
+    bad[0, 300] = float("nan")
+    bad[T - 1, 5] = float("inf")
+    out = lin(bad)
+    assert bool((~torch.isfinite(out[0])).all()) and bool((~torch.isfinite(out[T - 1])).all())
+    assert torch.equal(out[1:T - 1], clean[1:T - 1])
+
+
+def test_no_tokens(moe, cuda_device):
+    x, w, s, _ = make(0, 64, 64, 32, "f32", 1, False, cuda_device)
+    assert moe.linear_forward(x, w, s, 32).shape == (0, 64)
+
+
+def test_long_offsets(moe, cuda_device):
+    """Codes and outputs past 2^32 bytes: rows at both ends and around the borders."""
+    N, K, T = 300_000, 32768, 2
+    g = gen(3, cuda_device)
+    w = torch.randint(-2 ** 63, 2 ** 63 - 1, (N * K // 16,), generator=g, device=cuda_device).view(torch.uint8).view(N, K // 2)
+    s = scales(g, (N,), K, 128, "bf16")
+    x = torch.randn((T, K), generator=g, device=cuda_device).to(torch.bfloat16)
+    out = moe.linear_forward(x, w, s, 128)
+    edge = 2 ** 32 // (K // 2)  # the row that crosses 2^32 bytes
+    rows = torch.tensor([0, 1, edge // 2 - 1, edge // 2, edge - 1, edge, edge + 1, N - 17, N - 2, N - 1], device=cuda_device)
+    check(out[:, rows], x, w[rows], s[rows], 128)
+
+
+@pytest.mark.parametrize("T", [1, 6, 48])
+def test_two_calls_at_once(moe, cuda_device, T):
+    N, K = 3001, 2048
+    x, w, s, a = make(T, N, K, 128, "bf16", 4, True, cuda_device)
+    lin = moe.Int4Linear(w, s, 128)
+    want = lin(x, add=a)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [torch.empty_like(want) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, o in zip(streams, outs):
+            lin(x, out=o, add=a, stream=st)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("T", [1, 8, 70])
+def test_graph_replay(moe, cuda_device, T):
+    N, K = 500, 1024
+    x, w, s, _ = make(T, N, K, 32, "f16", 8, False, cuda_device)
+    lin = moe.Int4Linear(w, s, 32)
+    out = torch.empty((T, N), dtype=torch.bfloat16, device=cuda_device)
+    lin(x, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lin(x, out=out)
+    for seed in range(3):
+        x.copy_(make(T, N, K, 32, "f16", 80 + seed, False, cuda_device)[0])
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, x, w, s, 32)
+
+
+def test_binding_refusals(moe, cuda_device):
+    x, w, s, a = make(4, 64, 128, 32, "f32", 2, True, cuda_device)
+    lin = moe.Int4Linear(w, s, 32)
+    for bad in (x.float(), x[:, :96], x.cpu(), x[:1].expand(4, 128), x.t().contiguous().t()):
+        with pytest.raises(ValueError):
+            lin(bad)
+    with pytest.raises(ValueError):
+        lin(x, add=a[:2])
+    with pytest.raises(ValueError):
+        lin(x, out=torch.empty((4, 64), device=cuda_device))
+    for args in ((w, s[:, :3], 32), (w, s.double(), 32), (w.cpu(), s, 32), (w, s, 64), (w[:, ::2], s, 32)):
+        with pytest.raises(ValueError):
+            moe.Int4Linear(*args)
+    with pytest.raises(moe.MoeError):
+        moe.Int4Linear(w, scales(gen(0, cuda_device), (64,), 128, 48), 48)  # not a power of two
+    with pytest.raises(moe.MoeError):
+        lin(x, out=x[:, :64])  # overlaps x
