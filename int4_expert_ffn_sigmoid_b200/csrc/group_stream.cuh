@@ -1,0 +1,200 @@
+// Weight streaming of the group-scaled int4 operators (internal): one warp
+// multiplies 16 weight rows x 256 columns (a chunk: 2 KB of codes) with up to
+// eight tokens on mma.sync m16n8k32 s8.
+//
+// Activations.  A token's 256 columns of a chunk are written as s * (q0 + q1 /
+// 256) with int8 q0, q1 and a power of two s from their largest magnitude
+// (qscale): 16 bits, off by at most 2^-15 of that magnitude.  Columns 2j and
+// 2j + 1 of an mma's n-tile are the two parts of token j, so a tile serves
+// four tokens.  int8 instead of bf16 operands because a weight word then
+// reaches the mma in three logic operations per eight codes (lo8 / hi8;
+// eleven to bf16) and an mma covers twice the columns: at the copy rate of HBM
+// an SM has ~46 codes a cycle to convert.  The products sum exactly in int32
+// within a group: |256 sum(q0 c) + sum(q1 c)| < 2^31 for up to 256 columns.
+//
+// A chunk is staged in shared memory, 128 bytes a row, its 16-byte segments
+// permuted by the row (seg_perm), so that both fragment reads are free of
+// bank conflicts:
+//  - fine groups (32, 64 columns): lane (g, q) of an mma reads word q of a
+//    32-column block of rows g and g + 8 (all four lanes of a row in one group);
+//  - coarse groups (128 columns and more): it reads the 16 bytes of columns
+//    32 q of a 128-column half, whose four words go to four mmas; the
+//    activations are stored in that order (x_pos).
+#pragma once
+
+#include "group_int4.h"
+#include "stream_ops.cuh"
+
+namespace moe {
+
+constexpr int kChunkK = 256;
+constexpr int kStageBytes = 16 * kChunkK / 2;
+
+__device__ __forceinline__ int seg_perm(int row) { return ((row & 1) << 2) | ((row >> 1) & 3); }
+
+// Bytes of one part of one token's activations, `chunks` chunks long: the
+// padding puts the rows of a fragment read on different banks.
+template <bool kCoarse>
+__host__ __device__ constexpr int x_stride(int chunks) {
+    return chunks * kChunkK + (kCoarse ? 64 : 32);
+}
+
+// Byte offset, within its chunk, of the eight columns 8 i .. 8 i + 7.
+template <bool kCoarse>
+__device__ __forceinline__ int x_pos(int i) {
+    if (!kCoarse) return 8 * i;
+    return (i >> 4) * 128 + ((i & 3) >> 1) * 64 + ((i >> 2) & 3) * 16 + (i & 1) * 8;
+}
+
+// One chunk of one token (a warp; lane l holds columns 8 l .. 8 l + 7 as
+// bf16, zero past the row's end): both int8 parts to q0 / q1 (the chunk's
+// bytes of each part's row) in the byte order of lo8 / hi8, the scale of the
+// integer sums to *xs (2^-12 of qscale's: the weights enter as 16 c and part
+// 0 as 256 q0); NaN for a chunk that holds NaN or an infinity.
+template <bool kCoarse>
+__device__ __forceinline__ void quantize_chunk(uint4 v, int8_t* q0, int8_t* q1, float* xs, int lane) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16lo(w[i]);
+        f[2 * i + 1] = bf16hi(w[i]);
+        m = nanmax(nanmax(m, fabsf(f[2 * i])), fabsf(f[2 * i + 1]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = nanmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const QScale qs = qscale(m);
+    uint2 a, b;
+    quant2x8(f, qs, a, b);
+    *reinterpret_cast<uint2*>(q0 + x_pos<kCoarse>(lane)) = a;
+    *reinterpret_cast<uint2*>(q1 + x_pos<kCoarse>(lane)) = b;
+    if (lane == 0) *xs = qs.s * 0x1p-12f;
+}
+
+// Issues the copies of chunk columns [256 c, 256 c + 256) of 16 rows into a
+// stage (one warp).  `row` gives the address of a row's first code; segments
+// past the row's end (its length K is a multiple of 32) are left as they are:
+// their activations are zero, and the sums are of integers.
+template <typename Row>
+__device__ __forceinline__ void issue_chunk(uint8_t* stage, int c, int K, int lane, Row row) {
+    const int seg = lane & 7, r0 = lane >> 3;
+    if (c * kChunkK + seg * 32 < K) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 4 * i;
+            cp_async16(stage + r * 128 + ((seg ^ seg_perm(r)) << 4), row(r) + (size_t)c * (kChunkK / 2) + seg * 16);
+        }
+    }
+}
+
+// Scales of a chunk's groups for the two rows g, g + 8 of a lane's quad: lane
+// q holds groups q and q + 4 of either row (fine groups), or group q & 1
+// (coarse ones).  s0, s8: index of the rows' first scale.
+template <bool kCoarse>
+__device__ __forceinline__ void load_chunk_scales(float (&sc)[4], const void* s, size_t s0, size_t s8, int c, int gshift,
+                                                  int G, int stype, int q) {
+    if (kCoarse) {
+        const int i = min((c * kChunkK + (q & 1) * 128) >> gshift, G - 1);
+        sc[0] = load_scale(s, s0 + i, stype);
+        sc[2] = load_scale(s, s8 + i, stype);
+    } else {
+        const int first = (c * kChunkK) >> gshift;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = first + q + 4 * u;
+            const bool in = i < G && (u == 0 || gshift == 5);
+            sc[u] = in ? load_scale(s, s0 + i, stype) : 0.f;
+            sc[2 + u] = in ? load_scale(s, s8 + i, stype) : 0.f;
+        }
+    }
+}
+
+__device__ __forceinline__ void mma_s8_first(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+
+// t[n][0 / 1] += scale of row g / g + 8 times the joined integer sums.
+template <int NT>
+__device__ __forceinline__ void scale_group(float (&t)[NT][2], const int (&d)[NT][4], float s0, float s8) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        t[n][0] = fmaf((float)(d[n][0] * 256 + d[n][1]), s0, t[n][0]);
+        t[n][1] = fmaf((float)(d[n][2] * 256 + d[n][3]), s8, t[n][1]);
+    }
+}
+
+// One staged chunk times the tokens' chunk: t[n][0 / 1], for token 4 n + q
+// and rows g / g + 8, in units of the token's xs.  stage: shared address;
+// xb[n]: shared address of this lane's B row (token 4 n + g / 2, part g % 2)
+// at the chunk's start.
+template <int NT, bool kCoarse>
+__device__ __forceinline__ void chunk_mma(uint32_t stage, const uint32_t (&xb)[NT], const float (&sc)[4], int gshift,
+                                          int lane, float (&t)[NT][2]) {
+    const int g = lane >> 2, q = lane & 3, quad = lane & 28;
+    const uint32_t row = stage + g * 128 + (seg_perm(g) << 4);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) t[n][0] = t[n][1] = 0.f;
+    int d[NT][4];
+    if (kCoarse) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = row ^ ((4 * h + q) << 4);
+            const uint4 wa = lds128(at), wb = lds128(at + 1024);
+            const uint32_t u[4] = {wa.x, wa.y, wa.z, wa.w}, v[4] = {wb.x, wb.y, wb.z, wb.w};
+            uint4 b[NT];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a[4] = {lo8(u[j]), lo8(v[j]), hi8(u[j]), hi8(v[j])};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if ((j & 1) == 0) b[n] = lds128(xb[n] + h * 128 + (j >> 1) * 64 + q * 16);
+                    const uint32_t b0 = (j & 1) ? b[n].z : b[n].x, b1 = (j & 1) ? b[n].w : b[n].y;
+                    if (j == 0 && (h == 0 || gshift == 7)) mma_s8_first(d[n], a, b0, b1);
+                    else mma_s8(d[n], a, b0, b1);
+                }
+            }
+            if (h == 1 || gshift == 7)
+                scale_group<NT>(t, d, __shfl_sync(0xffffffffu, sc[0], quad | h), __shfl_sync(0xffffffffu, sc[2], quad | h));
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            const uint32_t at = (row ^ (b << 4)) + q * 4;
+            const uint32_t wa = lds32(at), wb = lds32(at + 1024);
+            const uint32_t a[4] = {lo8(wa), lo8(wb), hi8(wa), hi8(wb)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint2 x = lds64(xb[n] + 32 * b + 8 * q);
+                if ((b & 1) == 0 || gshift == 5) mma_s8_first(d[n], a, x.x, x.y);
+                else mma_s8(d[n], a, x.x, x.y);
+            }
+            if (gshift == 5)
+                scale_group<NT>(t, d, __shfl_sync(0xffffffffu, sc[b >> 2], quad | (b & 3)),
+                                __shfl_sync(0xffffffffu, sc[2 + (b >> 2)], quad | (b & 3)));
+            else if (b & 1)
+                scale_group<NT>(t, d, __shfl_sync(0xffffffffu, sc[0], quad | (b >> 1)),
+                                __shfl_sync(0xffffffffu, sc[2], quad | (b >> 1)));
+        }
+    }
+}
+
+}  // namespace moe

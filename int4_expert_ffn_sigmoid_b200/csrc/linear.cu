@@ -1,62 +1,205 @@
 // Dense projection with int4 weights and group scales:
 //   out[t][n] = sum_k x[t][k] c[n][k] s[n][k / group]  (+ add[t][n]).
-#include "group_int4.h"
+#include "group_stream.cuh"
 
 namespace moe {
 
-// Elements of word w of codes, in order.
-__device__ __forceinline__ float code_of(uint32_t w, int j) { return (float)((int)(w << (28 - 4 * j)) >> 28); }
+// Weight streaming for up to eight tokens a pass.  A CTA takes tiles of 16 *
+// wr rows; its warps are wr teams of wk, warp (team, j) multiplying the chunks
+// j, j + wk, ... of its team's 16 rows (chunk_mma) and the team's partial sums
+// meeting in shared memory.  Each warp runs its own ring of kDepth staged
+// chunks on cp.async (no barrier with another warp), across tile borders, and
+// fills it before waiting on the previous kernel: weights and scales are
+// constants, x and add are not.
+constexpr int kDepth = 3;
+constexpr int kPassTok = 8;
+// Dynamic shared memory of one CTA at most, and of the activations alone.
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kXMax = 112 * 1024;
 
-// A warp per output row, eight tokens at a time, f32 multiply-adds: lane l
-// takes the words (eight codes) l, l + 32, ... of the row.
-constexpr int kRowWarps = 8, kRowTok = 8;
+struct StreamPlan {
+    int wk, wr;        // warps along the columns, teams
+    int chunks, tiles; // 256-column chunks of a row; CTA tiles of 16 * wr rows
+    int t0, nt;        // the pass's first token and its tokens
+};
 
-__global__ void __launch_bounds__(32 * kRowWarps) linear_row_kernel(LinearArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long n = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    pdl_wait();
-    pdl_release();
-    if (n >= a.N) return;
-    const uint32_t* wr = reinterpret_cast<const uint32_t*>(a.w + (size_t)n * (a.K / 2));
-    for (long long t0 = (long long)blockIdx.y * kRowTok; t0 < a.T; t0 += (long long)gridDim.y * kRowTok) {
-        float acc[kRowTok] = {};
-        for (int i = lane; i < a.K / 8; i += 32) {
-            const uint32_t w = __ldg(wr + i);
-            const float s = load_scale(a.scales, (size_t)n * a.G + ((8 * i) >> a.gshift), a.stype);
-#pragma unroll
-            for (int u = 0; u < kRowTok; ++u) {
-                if (t0 + u >= a.T) break;
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.x + (t0 + u) * a.ldx) + i);
-                const uint32_t xs[4] = {v.x, v.y, v.z, v.w};
-                float p = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p = fmaf(code_of(w, 2 * j), bf16lo(xs[j]), p);
-                    p = fmaf(code_of(w, 2 * j + 1), bf16hi(xs[j]), p);
-                }
-                acc[u] = fmaf(s, p, acc[u]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kRowTok; ++u) {
-            if (t0 + u >= a.T) break;
-            float v = acc[u];
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) {
-                if (a.add) v += __bfloat162float(a.add[(t0 + u) * a.lda + n]);
-                if (a.out_f32) static_cast<float*>(a.out)[(t0 + u) * a.ldo + n] = v;
-                else static_cast<__nv_bfloat16*>(a.out)[(t0 + u) * a.ldo + n] = __float2bfloat16_rn(v);
-            }
-        }
-    }
+template <int NW>
+__host__ __device__ constexpr int red_floats(int ntok) {
+    return NW * 16 * ntok;
 }
 
-int linear_launches(const LinearArgs&) { return 1; }
+template <int NW, int NT, bool kCoarse>
+__global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel(LinearArgs a, StreamPlan p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int team = warp / p.wk, j = warp - team * p.wk;
+    const int g = lane >> 2, q = lane & 3;
+    const int xs_bytes = x_stride<kCoarse>(p.chunks);
+    uint8_t* ring = smem + warp * (kDepth * kStageBytes);
+    float* red = reinterpret_cast<float*>(smem + NW * kDepth * kStageBytes);  // [2][NW][4 NT][16]
+    float* xs = red + 2 * red_floats<NW>(4 * NT);                            // [chunks][4 NT]
+    int8_t* xq = reinterpret_cast<int8_t*>(xs + p.chunks * 4 * NT);          // [token][part][xs_bytes]
+
+    // this warp's chunks, tile after tile
+    const int per = j < p.chunks ? (p.chunks - j + p.wk - 1) / p.wk : 0;
+    const int tiles = p.tiles > (int)blockIdx.x ? (p.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    const long long total = (long long)per * tiles;
+    auto first_row = [&](int i) { return ((long long)blockIdx.x + (long long)i * gridDim.x) * 16 * p.wr + team * 16; };
+    auto clamp_row = [&](long long r) { return (size_t)(r < a.N ? r : a.N - 1); };
+    int it = 0, ic = 0;  // tile and chunk of the next copy
+    long long issued = 0;
+    auto issue = [&]() {
+        if (issued < total) {
+            const long long r0 = first_row(it);
+            issue_chunk(ring + (issued % kDepth) * kStageBytes, j + ic * p.wk, a.K, lane,
+                        [&](int r) { return a.w + clamp_row(r0 + r) * (a.K / 2); });
+            if (++ic == per) {
+                ic = 0;
+                ++it;
+            }
+        }
+        ++issued;
+        cp_async_commit();
+    };
+    float nxt[4];
+    auto scales = [&](int i, int c) {
+        const long long r0 = first_row(i);
+        load_chunk_scales<kCoarse>(nxt, a.scales, clamp_row(r0 + g) * a.G, clamp_row(r0 + g + 8) * a.G, j + c * p.wk,
+                                   a.gshift, a.G, a.stype, q);
+    };
+    for (int i = 0; i < kDepth; ++i) issue();
+    if (total > 0) scales(0, 0);
+    pdl_wait();
+    pdl_release();
+
+    for (int i = warp; i < p.nt * p.chunks; i += NW) {
+        const int t = i / p.chunks, c = i - t * p.chunks;
+        const int k = c * kChunkK + 8 * lane;
+        const uint4 v = k < a.K ? __ldg(reinterpret_cast<const uint4*>(a.x + (p.t0 + t) * a.ldx + k)) : make_uint4(0, 0, 0, 0);
+        int8_t* r = xq + (size_t)2 * t * xs_bytes + c * kChunkK;
+        quantize_chunk<kCoarse>(v, r, r + xs_bytes, xs + c * 4 * NT + t, lane);
+    }
+    __syncthreads();
+
+    uint32_t xrow[NT];  // a column past the last token repeats it: its sums are not stored
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int t = min(4 * n + (g >> 1), p.nt - 1);
+        xrow[n] = smem_addr(xq + (size_t)(2 * t + (g & 1)) * xs_bytes);
+    }
+    const uint32_t ring_at = smem_addr(ring);
+    long long done = 0;
+    for (int i = 0; i < tiles; ++i) {
+        float acc[NT][2] = {};
+        for (int c = 0; c < per; ++c) {
+            float sc[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sc[u] = nxt[u];
+            if (c + 1 < per) scales(i, c + 1);
+            else if (i + 1 < tiles) scales(i + 1, 0);
+            cp_async_wait<kDepth - 1>();
+            __syncwarp();
+            const int ch = j + c * p.wk;
+            uint32_t xb[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) xb[n] = xrow[n] + ch * kChunkK;
+            float t[NT][2];
+            chunk_mma<NT, kCoarse>(ring_at + (int)(done % kDepth) * kStageBytes, xb, sc, a.gshift, lane, t);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float s = xs[ch * 4 * NT + min(4 * n + q, p.nt - 1)];
+                acc[n][0] = fmaf(t[n][0], s, acc[n][0]);
+                acc[n][1] = fmaf(t[n][1], s, acc[n][1]);
+            }
+            ++done;
+            __syncwarp();
+            issue();
+        }
+        float* part = red + (i & 1) * red_floats<NW>(4 * NT);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float* o = part + (warp * 4 * NT + 4 * n + q) * 16;
+            o[g] = acc[n][0];
+            o[g + 8] = acc[n][1];
+        }
+        __syncthreads();
+        for (int o = tid; o < p.nt * p.wr * 16; o += 32 * NW) {
+            const int r = o & 15, tm = (o >> 4) % p.wr, t = (o >> 4) / p.wr;
+            const long long n = ((long long)blockIdx.x + (long long)i * gridDim.x) * 16 * p.wr + tm * 16 + r;
+            if (n >= a.N) continue;
+            float v = 0.f;
+            for (int u = 0; u < p.wk; ++u) v += part[((tm * p.wk + u) * 4 * NT + t) * 16 + r];
+            const long long tt = p.t0 + t;
+            if (a.add) v += __bfloat162float(a.add[tt * a.lda + n]);
+            if (a.out_f32) static_cast<float*>(a.out)[tt * a.ldo + n] = v;
+            else static_cast<__nv_bfloat16*>(a.out)[tt * a.ldo + n] = __float2bfloat16_rn(v);
+        }
+    }
+    cp_async_wait<0>();
+}
+
+namespace {
+
+int sms() {
+    static int cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    if (cache[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        cache[dev] = n;
+    }
+    return cache[dev];
+}
+
+template <int NW, int NT, bool kCoarse>
+cudaError_t launch_pass(const LinearArgs& a, StreamPlan p, cudaStream_t stream) {
+    const size_t smem = (size_t)NW * kDepth * kStageBytes + 2 * red_floats<NW>(4 * NT) * 4 + (size_t)p.chunks * 4 * NT * 4 +
+                        (size_t)p.nt * 2 * x_stride<kCoarse>(p.chunks);
+    auto* k = linear_stream_kernel<NW, NT, kCoarse>;
+    static int set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && !set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        if (e != cudaSuccess) return e;
+        set[dev] = 1;
+    }
+    const int per_sm = NW == 8 ? (3 * smem <= kSmemMax - 3 * 1024 ? 3 : 2 * smem <= kSmemMax - 2 * 1024 ? 2 : 1) : 1;
+    p.tiles = (a.N + 16 * p.wr - 1) / (16 * p.wr);
+    const int grid = p.tiles < per_sm * sms() ? p.tiles : per_sm * sms();
+    return launch_pdl(k, dim3(grid), dim3(32 * NW), smem, stream, a, p);
+}
+
+template <int NW>
+cudaError_t launch_pass(const LinearArgs& a, const StreamPlan& p, cudaStream_t stream) {
+    const bool coarse = a.gshift >= 7;
+    if (p.nt <= 4) return coarse ? launch_pass<NW, 1, true>(a, p, stream) : launch_pass<NW, 1, false>(a, p, stream);
+    return coarse ? launch_pass<NW, 2, true>(a, p, stream) : launch_pass<NW, 2, false>(a, p, stream);
+}
+
+int pass_tokens(const LinearArgs& a) {
+    const int fit = kXMax / (2 * x_stride<true>((a.K + kChunkK - 1) / kChunkK));
+    return fit < kPassTok ? fit : kPassTok;
+}
+
+}  // namespace
+
+int linear_launches(const LinearArgs& a) { return (a.T + pass_tokens(a) - 1) / pass_tokens(a); }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
-    const int gy = (a.T + kRowTok - 1) / kRowTok;
-    return launch_pdl(linear_row_kernel, dim3((a.N + kRowWarps - 1) / kRowWarps, gy < 65535 ? gy : 65535),
-                      dim3(32 * kRowWarps), 0, stream, a);
+    StreamPlan p = {};
+    p.chunks = (a.K + kChunkK - 1) / kChunkK;
+    const int pass = pass_tokens(a);
+    for (p.t0 = 0; p.t0 < a.T; p.t0 += pass) {
+        p.nt = a.T - p.t0 < pass ? a.T - p.t0 : pass;
+        const int nw = p.nt <= 2 ? 8 : 16;
+        for (p.wk = 1; p.wk < nw && p.wk < p.chunks; p.wk *= 2) {}
+        if (p.wk > 8 && nw == 16 && p.chunks < 32) p.wk = 8;
+        p.wr = nw / p.wk;
+        const cudaError_t e = nw == 8 ? launch_pass<8>(a, p, stream) : launch_pass<16>(a, p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace moe
