@@ -10,6 +10,7 @@ The C ABI is declared in ``include/moe_int4.h``; the names here mirror it.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -456,19 +457,29 @@ def _scale_shape(rows, cols: int, group: int) -> tuple:
     return (*rows, -(-cols // group)) if group else tuple(rows)
 
 
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on_device(device: torch.device):
+    """A context in which ``device`` is the current one (calls are short: no switch when it is already)."""
+    return _NO_GUARD if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+
+
 def _raw_stream(device: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream of {stream.device} for tensors on {device}")
         return stream.cuda_stream
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _rows_of(name: str, t: torch.Tensor, dtypes, shape, device) -> int:
-    """The elements between rows of a 2-D tensor whose rows are contiguous (any distance for one row)."""
-    if not t.is_cuda or t.device != device or t.dtype not in dtypes or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected a {' or '.join(map(str, dtypes))} tensor of shape {shape} on {device}, "
+def _rows_of(name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """The elements between rows of a 2-D tensor whose rows are contiguous (0: their length)."""
+    if t.device != device or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {shape} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return 0
     if shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: expected contiguous rows, got strides {t.stride()}")
     if shape[0] > 1:
@@ -496,6 +507,7 @@ class Int4Linear:
         if scales.device != w.device:
             raise ValueError(f"w is on {w.device}, scales on {scales.device}")
         self.w, self.scales, self.device = w, scales, w.device
+        self._w, self._s = w.data_ptr(), scales.data_ptr()
         self.cfg = moe_linear_cfg_t(struct_size=ctypes.sizeof(moe_linear_cfg_t), N=self.N, K=self.K, group=self.group,
                                     scale_type=_scale_type("scales", scales))
         if lib.moe_linear_kernel_launches(ctypes.byref(self.cfg), 1) == 0:
@@ -505,24 +517,25 @@ class Int4Linear:
                  flags: int = 0, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """out[t] = W x[t] (+ add[t]).  x: bfloat16 [T, K], add: bfloat16 [T, N], out: bfloat16 (float32 under
         MOE_OUT_F32) [T, N]; each may have rows further apart than their length.  ``out`` may be ``add``."""
-        T = x.shape[0]
-        c = moe_linear_cfg_t.from_buffer_copy(self.cfg)
-        c.flags = flags
+        T, device = x.shape[0], self.device
         odt = torch.float32 if flags & MOE_OUT_F32 else torch.bfloat16
-        c.ldx = _rows_of("x", x, (torch.bfloat16,), (T, self.K), self.device)
+        ldx, ldo, lda, ap = _rows_of("x", x, torch.bfloat16, (T, self.K), device), 0, 0, None
         if out is None:
-            out = torch.empty((T, self.N), dtype=odt, device=self.device)
+            out = x.new_empty((T, self.N)) if not flags else x.new_empty((T, self.N), dtype=odt)
         else:
-            c.ldo = _rows_of("out", out, (odt,), (T, self.N), self.device)
-        ap = None
+            ldo = _rows_of("out", out, odt, (T, self.N), device)
         if add is not None:
-            c.lda = _rows_of("add", add, (torch.bfloat16,), (T, self.N), self.device)
+            lda = _rows_of("add", add, torch.bfloat16, (T, self.N), device)
             ap = add.data_ptr()
         if T == 0:
             return out
-        with torch.cuda.device(self.device):
-            st = lib.moe_linear_forward(x.data_ptr(), self.w.data_ptr(), self.scales.data_ptr(), ap, out.data_ptr(),
-                                        T, ctypes.byref(c), _raw_stream(self.device, stream))
+        c = self.cfg
+        if ldx or ldo or lda or flags:
+            c = moe_linear_cfg_t.from_buffer_copy(c)
+            c.ldx, c.ldo, c.lda, c.flags = ldx, ldo, lda, flags
+        with _on_device(device):
+            st = lib.moe_linear_forward(x.data_ptr(), self._w, self._s, ap, out.data_ptr(), T, ctypes.byref(c),
+                                        _raw_stream(device, stream))
         if st != MOE_OK:
             raise MoeError(st, "moe_linear_forward")
         return out
@@ -599,6 +612,11 @@ class MoEFewLayer:
     def new_workspace(self) -> torch.Tensor:
         return torch.empty_like(self.workspace)
 
+    def _check(self, name, t, dtype, shape):
+        if t.device != self.device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
     def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, residual: bool = False, flags: int = 0,
                  topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
@@ -609,16 +627,16 @@ class MoEFewLayer:
         f = flags | (MOE_ADD_RESIDUAL if residual else 0)
         odt = torch.float32 if f & MOE_OUT_F32 else torch.bfloat16
         if out is None:
-            out = torch.empty((T, shape.H), dtype=odt, device=self.device)
+            out = x.new_empty((T, shape.H), dtype=odt, device=self.device)
         ws = self.workspace if workspace is None else workspace
-        for name, t, dt, sh in (("x", x, torch.bfloat16, (T, shape.H)), ("out", out, odt, (T, shape.H)),
-                                ("topk_idx", topk_idx, torch.int32, (T, shape.K)),
-                                ("topk_w", topk_w, torch.float32, (T, shape.K)), ("workspace", ws, torch.uint8, None)):
-            if t is None:
-                continue
-            _check_dev(name, t, dt, sh)
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the layer on {self.device}")
+        self._check("x", x, torch.bfloat16, (T, shape.H))
+        self._check("out", out, odt, (T, shape.H))
+        if topk_idx is not None:
+            self._check("topk_idx", topk_idx, torch.int32, (T, shape.K))
+        if topk_w is not None:
+            self._check("topk_w", topk_w, torch.float32, (T, shape.K))
+        if workspace is not None:
+            self._check("workspace", ws, torch.uint8, ws.shape)
         if T == 0:
             return out
         c = moe_few_cfg_t.from_buffer_copy(self.cfg)
@@ -626,7 +644,7 @@ class MoEFewLayer:
         c.workspace, c.workspace_bytes = ws.data_ptr(), ws.numel()
         c.topk_idx_out = None if topk_idx is None else topk_idx.data_ptr()
         c.topk_w_out = None if topk_w is None else topk_w.data_ptr()
-        with torch.cuda.device(self.device):
+        with _on_device(self.device):
             st = lib.moe_few_forward(x.data_ptr(), ctypes.byref(self.weights), out.data_ptr(), T, ctypes.byref(c),
                                      _raw_stream(self.device, stream))
         if st != MOE_OK:

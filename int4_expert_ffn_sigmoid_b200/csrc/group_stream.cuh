@@ -46,44 +46,77 @@ __device__ __forceinline__ int x_pos(int i) {
     return (i >> 4) * 128 + ((i & 3) >> 1) * 64 + ((i >> 2) & 3) * 16 + (i & 1) * 8;
 }
 
+// Scale of 256 values whose largest magnitude has the bf16 bits m (sign
+// cleared): *s = 2^e with |v| / 2^e <= 127, *inv = 256 / s.  Magnitudes below
+// 2^-113 (e clamped at -119) become zero; NaN for NaN and infinity.
+__device__ __forceinline__ void block_scale(uint32_t m, float* s, float* inv) {
+    // |v| / 2^e in [64, 127]: the largest significand, 127.5 / 64, takes the next e
+    const int e = max((int)(m >> 7) - 133 + ((m & 127) == 127), -119);
+    *s = m >= 0x7f80 ? __int_as_float(0x7fc00000) : __int_as_float((e + 127) << 23);
+    *inv = __int_as_float((135 - e) << 23);
+}
+
+// v * inv (inv = 256 / s, |v| <= 127 s) rounded to the nearest integer q: the
+// addition of 1.5 * 2^23 leaves q in the low bits.  Byte 0 is q1 (signed);
+// byte 1 of the sum with 128 is q0, q = 256 q0 + q1.
+__device__ __forceinline__ uint32_t fixed16(float v, float inv) { return __float_as_uint(fmaf(v, inv, 12582912.f)); }
+
+// Eight fixed16 values to the bytes of both parts, in the order of lo8 / hi8
+// (0, 2, 4, 6, 1, 3, 5, 7).
+__device__ __forceinline__ void pack_parts(const uint32_t (&f)[8], uint2& p0, uint2& p1) {
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = f[i] + 128;
+    auto low = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+        return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    };
+    auto high = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+        return __byte_perm(__byte_perm(a, b, 0x0051), __byte_perm(c, d, 0x0051), 0x5410);
+    };
+    p0 = make_uint2(high(h[0], h[2], h[4], h[6]), high(h[1], h[3], h[5], h[7]));
+    p1 = make_uint2(low(f[0], f[2], f[4], f[6]), low(f[1], f[3], f[5], f[7]));
+}
+
 // One chunk of one token (a warp; lane l holds columns 8 l .. 8 l + 7 as
 // bf16, zero past the row's end): both int8 parts to q0 / q1 (the chunk's
-// bytes of each part's row) in the byte order of lo8 / hi8, the scale of the
-// integer sums to *xs (2^-12 of qscale's: the weights enter as 16 c and part
-// 0 as 256 q0); NaN for a chunk that holds NaN or an infinity.
+// bytes of each part's row), the scale of the integer sums to *xs (2^-12 of
+// the block's: the weights enter as 16 c, part 0 as 256 q0); NaN for a chunk
+// that holds NaN or an infinity.
 template <bool kCoarse>
 __device__ __forceinline__ void quantize_chunk(uint4 v, int8_t* q0, int8_t* q1, float* xs, int lane) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float f[8], m = 0.f;
+    const uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                 __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+    float s, inv;
+    block_scale(m, &s, &inv);
+    uint32_t f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16lo(w[i]);
-        f[2 * i + 1] = bf16hi(w[i]);
-        m = nanmax(nanmax(m, fabsf(f[2 * i])), fabsf(f[2 * i + 1]));
+        f[2 * i] = fixed16(bf16lo(w[i]), inv);
+        f[2 * i + 1] = fixed16(bf16hi(w[i]), inv);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = nanmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const QScale qs = qscale(m);
     uint2 a, b;
-    quant2x8(f, qs, a, b);
+    pack_parts(f, a, b);
     *reinterpret_cast<uint2*>(q0 + x_pos<kCoarse>(lane)) = a;
     *reinterpret_cast<uint2*>(q1 + x_pos<kCoarse>(lane)) = b;
-    if (lane == 0) *xs = qs.s * 0x1p-12f;
+    if (lane == 0) *xs = s * 0x1p-12f;
 }
 
-// Issues the copies of chunk columns [256 c, 256 c + 256) of 16 rows into a
-// stage (one warp).  `row` gives the address of a row's first code; segments
-// past the row's end (its length K is a multiple of 32) are left as they are:
-// their activations are zero, and the sums are of integers.
-template <typename Row>
-__device__ __forceinline__ void issue_chunk(uint8_t* stage, int c, int K, int lane, Row row) {
-    const int seg = lane & 7, r0 = lane >> 3;
-    if (c * kChunkK + seg * 32 < K) {
+// Issues the copies of a chunk of 16 rows into a stage (one warp).  Lane l
+// copies segment l % 8 of rows l / 8 + 4 i, i < 4, from p + off[i] (p: the
+// segment's place in the first row); `in`: the segment is inside the row.
+// Segments past a row's end are left as they are: their activations are zero,
+// and the sums are of integers.
+__device__ __forceinline__ void issue_chunk(uint32_t stage, const uint8_t* p, const int (&off)[4], bool in, int lane) {
+    if (in) {
+        const int seg = lane & 7, r0 = lane >> 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 4 * i;
-            cp_async16(stage + r * 128 + ((seg ^ seg_perm(r)) << 4), row(r) + (size_t)c * (kChunkK / 2) + seg * 16);
-        }
+        for (int i = 0; i < 4; ++i)
+            asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(
+                             stage + (r0 + 4 * i) * 128 + ((seg ^ seg_perm(r0 + 4 * i)) << 4)),
+                         "l"(p + off[i])
+                         : "memory");
     }
 }
 

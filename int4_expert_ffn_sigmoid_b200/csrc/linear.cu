@@ -18,9 +18,9 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kXMax = 112 * 1024;
 
 struct StreamPlan {
-    int wk, wr;        // warps along the columns, teams
-    int chunks, tiles; // 256-column chunks of a row; CTA tiles of 16 * wr rows
-    int t0, nt;        // the pass's first token and its tokens
+    int wk_log, wr_log;  // warps along the columns, teams: 1 << each
+    int chunks, tiles;   // 256-column chunks of a row; CTA tiles of 16 rows a team
+    int t0, nt;          // the pass's first token and its tokens
 };
 
 template <int NW>
@@ -32,86 +32,100 @@ template <int NW, int NT, bool kCoarse>
 __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel(LinearArgs a, StreamPlan p) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int team = warp / p.wk, j = warp - team * p.wk;
+    const int wk = 1 << p.wk_log, team = warp >> p.wk_log, j = warp & (wk - 1);
     const int g = lane >> 2, q = lane & 3;
     const int xs_bytes = x_stride<kCoarse>(p.chunks);
-    uint8_t* ring = smem + warp * (kDepth * kStageBytes);
     float* red = reinterpret_cast<float*>(smem + NW * kDepth * kStageBytes);  // [2][NW][4 NT][16]
     float* xs = red + 2 * red_floats<NW>(4 * NT);                            // [chunks][4 NT]
     int8_t* xq = reinterpret_cast<int8_t*>(xs + p.chunks * 4 * NT);          // [token][part][xs_bytes]
+    const uint32_t ring = smem_addr(smem + warp * (kDepth * kStageBytes));
 
     // this warp's chunks, tile after tile
-    const int per = j < p.chunks ? (p.chunks - j + p.wk - 1) / p.wk : 0;
-    const int tiles = p.tiles > (int)blockIdx.x ? (p.tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-    const long long total = (long long)per * tiles;
-    auto first_row = [&](int i) { return ((long long)blockIdx.x + (long long)i * gridDim.x) * 16 * p.wr + team * 16; };
-    auto clamp_row = [&](long long r) { return (size_t)(r < a.N ? r : a.N - 1); };
-    int it = 0, ic = 0;  // tile and chunk of the next copy
-    long long issued = 0;
+    const int per = j < p.chunks ? ((p.chunks - j - 1) >> p.wk_log) + 1 : 0;
+    const int tiles = p.tiles > (int)blockIdx.x ? (p.tiles - blockIdx.x - 1) / gridDim.x + 1 : 0;
+    const int rows_cta = 16 << p.wr_log, last = a.N - 1, half = a.K / 2;
+    int left = per * tiles;  // copies to issue
+
+    int ir = blockIdx.x * rows_cta + team * 16, ic = j;  // row and chunk of the next copy
+    int off[4], islot = 0;
+    const uint8_t* ip;
+    auto tile_offsets = [&]() {  // rows past the last repeat it: their sums are not stored
+        const int r0 = min(ir, last);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) off[i] = (min(ir + (lane >> 3) + 4 * i, last) - r0) * half;
+        ip = a.w + (size_t)r0 * half + (lane & 7) * 16;
+    };
     auto issue = [&]() {
-        if (issued < total) {
-            const long long r0 = first_row(it);
-            issue_chunk(ring + (issued % kDepth) * kStageBytes, j + ic * p.wk, a.K, lane,
-                        [&](int r) { return a.w + clamp_row(r0 + r) * (a.K / 2); });
-            if (++ic == per) {
-                ic = 0;
-                ++it;
+        if (left > 0) {
+            --left;
+            issue_chunk(ring + islot * kStageBytes, ip + ic * (kChunkK / 2), off, ic * kChunkK + (lane & 7) * 32 < a.K, lane);
+            islot = islot == kDepth - 1 ? 0 : islot + 1;
+            ic += wk;
+            if (ic >= p.chunks) {
+                ic = j;
+                ir += rows_cta * gridDim.x;
+                tile_offsets();
             }
         }
-        ++issued;
         cp_async_commit();
     };
     float nxt[4];
-    auto scales = [&](int i, int c) {
-        const long long r0 = first_row(i);
-        load_chunk_scales<kCoarse>(nxt, a.scales, clamp_row(r0 + g) * a.G, clamp_row(r0 + g + 8) * a.G, j + c * p.wk,
+    auto scales = [&](int row, int c) {
+        load_chunk_scales<kCoarse>(nxt, a.scales, (size_t)min(row + g, last) * a.G, (size_t)min(row + g + 8, last) * a.G, c,
                                    a.gshift, a.G, a.stype, q);
     };
+    int row = ir;
+    tile_offsets();
     for (int i = 0; i < kDepth; ++i) issue();
-    if (total > 0) scales(0, 0);
+    if (per > 0 && tiles > 0) scales(row, j);
     pdl_wait();
     pdl_release();
 
-    for (int i = warp; i < p.nt * p.chunks; i += NW) {
-        const int t = i / p.chunks, c = i - t * p.chunks;
+    for (int t = 0, c = warp; t < p.nt;) {
+        if (c >= p.chunks) {
+            c -= p.chunks;
+            ++t;
+            continue;
+        }
         const int k = c * kChunkK + 8 * lane;
         const uint4 v = k < a.K ? __ldg(reinterpret_cast<const uint4*>(a.x + (p.t0 + t) * a.ldx + k)) : make_uint4(0, 0, 0, 0);
-        int8_t* r = xq + (size_t)2 * t * xs_bytes + c * kChunkK;
+        int8_t* r = xq + 2 * t * xs_bytes + c * kChunkK;
         quantize_chunk<kCoarse>(v, r, r + xs_bytes, xs + c * 4 * NT + t, lane);
+        c += NW;
     }
     __syncthreads();
 
     uint32_t xrow[NT];  // a column past the last token repeats it: its sums are not stored
+    const float* xsc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int t = min(4 * n + (g >> 1), p.nt - 1);
-        xrow[n] = smem_addr(xq + (size_t)(2 * t + (g & 1)) * xs_bytes);
+        xrow[n] = smem_addr(xq + (2 * t + (g & 1)) * xs_bytes);
+        xsc[n] = xs + min(4 * n + q, p.nt - 1);
     }
-    const uint32_t ring_at = smem_addr(ring);
-    long long done = 0;
-    for (int i = 0; i < tiles; ++i) {
+    int slot = 0;
+    for (int i = 0; i < tiles; ++i, row += rows_cta * gridDim.x) {
         float acc[NT][2] = {};
-        for (int c = 0; c < per; ++c) {
+        for (int c = j; c < p.chunks; c += wk) {
             float sc[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) sc[u] = nxt[u];
-            if (c + 1 < per) scales(i, c + 1);
-            else if (i + 1 < tiles) scales(i + 1, 0);
+            if (c + wk < p.chunks) scales(row, c + wk);
+            else if (i + 1 < tiles) scales(row + rows_cta * gridDim.x, j);
             cp_async_wait<kDepth - 1>();
             __syncwarp();
-            const int ch = j + c * p.wk;
             uint32_t xb[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) xb[n] = xrow[n] + ch * kChunkK;
+            for (int n = 0; n < NT; ++n) xb[n] = xrow[n] + c * kChunkK;
             float t[NT][2];
-            chunk_mma<NT, kCoarse>(ring_at + (int)(done % kDepth) * kStageBytes, xb, sc, a.gshift, lane, t);
+            chunk_mma<NT, kCoarse>(ring + slot * kStageBytes, xb, sc, a.gshift, lane, t);
+            slot = slot == kDepth - 1 ? 0 : slot + 1;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float s = xs[ch * 4 * NT + min(4 * n + q, p.nt - 1)];
+                const float s = xsc[n][c * 4 * NT];
                 acc[n][0] = fmaf(t[n][0], s, acc[n][0]);
                 acc[n][1] = fmaf(t[n][1], s, acc[n][1]);
             }
-            ++done;
             __syncwarp();
             issue();
         }
@@ -123,12 +137,12 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
             o[g + 8] = acc[n][1];
         }
         __syncthreads();
-        for (int o = tid; o < p.nt * p.wr * 16; o += 32 * NW) {
-            const int r = o & 15, tm = (o >> 4) % p.wr, t = (o >> 4) / p.wr;
-            const long long n = ((long long)blockIdx.x + (long long)i * gridDim.x) * 16 * p.wr + tm * 16 + r;
+        for (int o = tid; o < (p.nt * 16 << p.wr_log); o += 32 * NW) {
+            const int r = o & 15, tm = (o >> 4) & ((1 << p.wr_log) - 1), t = o >> (4 + p.wr_log);
+            const int n = row - team * 16 + tm * 16 + r;
             if (n >= a.N) continue;
             float v = 0.f;
-            for (int u = 0; u < p.wk; ++u) v += part[((tm * p.wk + u) * 4 * NT + t) * 16 + r];
+            for (int u = 0; u < wk; ++u) v += part[(((tm << p.wk_log) + u) * 4 * NT + t) * 16 + r];
             const long long tt = p.t0 + t;
             if (a.add) v += __bfloat162float(a.add[tt * a.lda + n]);
             if (a.out_f32) static_cast<float*>(a.out)[tt * a.ldo + n] = v;
@@ -165,7 +179,7 @@ cudaError_t launch_pass(const LinearArgs& a, StreamPlan p, cudaStream_t stream) 
         set[dev] = 1;
     }
     const int per_sm = NW == 8 ? (3 * smem <= kSmemMax - 3 * 1024 ? 3 : 2 * smem <= kSmemMax - 2 * 1024 ? 2 : 1) : 1;
-    p.tiles = (a.N + 16 * p.wr - 1) / (16 * p.wr);
+    p.tiles = (a.N + (16 << p.wr_log) - 1) >> (4 + p.wr_log);
     const int grid = p.tiles < per_sm * sms() ? p.tiles : per_sm * sms();
     return launch_pdl(k, dim3(grid), dim3(32 * NW), smem, stream, a, p);
 }
@@ -192,11 +206,11 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
     const int pass = pass_tokens(a);
     for (p.t0 = 0; p.t0 < a.T; p.t0 += pass) {
         p.nt = a.T - p.t0 < pass ? a.T - p.t0 : pass;
-        const int nw = p.nt <= 2 ? 8 : 16;
-        for (p.wk = 1; p.wk < nw && p.wk < p.chunks; p.wk *= 2) {}
-        if (p.wk > 8 && nw == 16 && p.chunks < 32) p.wk = 8;
-        p.wr = nw / p.wk;
-        const cudaError_t e = nw == 8 ? launch_pass<8>(a, p, stream) : launch_pass<16>(a, p, stream);
+        const int nw_log = p.nt <= 2 ? 3 : 4;
+        for (p.wk_log = 0; p.wk_log < nw_log && (1 << p.wk_log) < p.chunks; ++p.wk_log) {}
+        if (p.wk_log > 3 && p.chunks < 32) p.wk_log = 3;
+        p.wr_log = nw_log - p.wk_log;
+        const cudaError_t e = nw_log == 3 ? launch_pass<8>(a, p, stream) : launch_pass<16>(a, p, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
