@@ -1,130 +1,619 @@
-// A whole MoE layer for a few tokens, with group-scaled int4 weights.
-#include "group_int4.h"
+// A whole MoE layer for a few tokens, with group-scaled int4 weights, in two
+// kernels (three when the router weights are large):
+//
+//   few_gate_up_kernel  router logits, selection, and h = silu(g) * u of every
+//                       touched expert and of the shared one
+//   few_down_kernel     the down projections, their weighted sum, the residual
+//
+// Both read each touched expert's weights once for all its tokens (group_stream.cuh)
+// and let the columns of an mma tile be the tokens themselves: token t is
+// column pair t of every expert's product, whether it picked the expert or
+// not, so nothing is gathered and the down kernel adds all experts of a row up
+// in registers.  A tile of four tokens that no pick touches is skipped, a
+// token that did not pick the expert is left out of the sum.
+//
+// h is stored as the down kernel's int8 operands: per 32 columns two int8
+// parts and a power-of-two scale (2^-15 of the block's largest value), taken
+// in f32 from the finished, routing-weighted h.
+#include <cooperative_groups.h>
+
+#include "group_stream.cuh"
+#include "moe_launch.h"
 
 namespace moe {
 
-__device__ __forceinline__ float few_sum(float v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
+constexpr int kFewTok = 8;
+constexpr int kFewWarps = 16;
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kFewDepth = 3;
+constexpr int kFewTileRows = 32;  // h elements of a gate/up tile
+constexpr int kFewMaxU = kFewTok * kMaxK;
+constexpr int kFewSmemMax = 227 * 1024;
+constexpr int kFewXMax = 98 * 1024;
+// CTAs that share the router: a cluster of kFewCluster computes all logits,
+// each CTA those of a quarter of the experts, and exchanges them in shared
+// memory.  Clusters of four leave 132 of 148 SMs usable, of eight 120.
+// Router weights beyond kFewRouterMax per CTA run as a kernel of their own in
+// front (router_logits_kernel), and every SM takes part in this one.
+constexpr int kFewCluster = 4;
+constexpr int kFewRouterMax = 128 * 1024;
 
-// Routing of one token (one CTA): logits, scores, the K largest keys.
-__global__ void __launch_bounds__(256) few_route_kernel(FewArgs a) {
-    __shared__ float s_score[kMaxE], s_key[kMaxE];
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
-    pdl_release();
-    for (int e = warp; e < a.E; e += 8) {
-        float acc = 0.f;
-        for (int h = lane; h < a.H; h += 32)
-            acc = fmaf(__bfloat162float(a.x[(size_t)t * a.H + h]), __ldg(a.rw + (size_t)e * a.H + h), acc);
-        acc = few_sum(acc);
-        if (lane == 0) {
-            const float s = 1.0f / (1.0f + expf(-acc)), k = s + a.rb[e];
-            s_score[e] = s;
-            s_key[e] = isnan(k) ? -INFINITY : k;
-        }
+bool few_split_router(int E, int H) { return (size_t)E * H * 4 > (size_t)kFewCluster * kFewRouterMax; }
+int few_logit_slices(int H) { return (H / 128 + 2) / 3; }
+
+// What the picks of a pass come to, in shared memory.
+struct FewPicks {
+    unsigned mask[kMaxE / 32];       // touched experts
+    int U;                           // their number
+    int expert[kFewMaxU];            // ascending
+    int8_t slot[kFewMaxU][kFewTok];  // t * K + k of token t's pick of the expert, or -1
+    float weight[kFewMaxU][kFewTok];
+    unsigned tokens[kFewMaxU];       // bit t: token t picked it
+};
+
+// Builds P from the picks (idx, wts: T * K <= 64 values, one per thread of the
+// first two warps; -1: dropped).  All threads of the CTA.
+__device__ __forceinline__ void few_gather(FewPicks& P, int T, int K, int my_e, float my_w) {
+    const int tid = threadIdx.x;
+    if (tid < kMaxE / 32) P.mask[tid] = 0;
+    __syncthreads();
+    const bool mine = tid < T * K && my_e >= 0;
+    if (mine) atomicOr(&P.mask[my_e >> 5], 1u << (my_e & 31));
+    for (int i = tid; i < kFewMaxU * kFewTok; i += kFewThreads) P.slot[i / kFewTok][i % kFewTok] = -1;
+    if (tid < kFewMaxU) P.tokens[tid] = 0;
+    __syncthreads();
+    auto rank = [&](int e) {
+        int r = 0;
+        for (int i = 0; i < (e >> 5); ++i) r += __popc(P.mask[i]);
+        return r + __popc(P.mask[e >> 5] & ((1u << (e & 31)) - 1));
+    };
+    if (mine) {
+        const int u = rank(my_e), t = tid / K;
+        P.expert[u] = my_e;
+        P.slot[u][t] = (int8_t)tid;
+        P.weight[u][t] = my_w;
+        atomicOr(&P.tokens[u], 1u << t);
+    }
+    if (tid == 0) {
+        int n = 0;
+        for (int i = 0; i < kMaxE / 32; ++i) n += __popc(P.mask[i]);
+        P.U = n;
     }
     __syncthreads();
-    if (warp != 0) return;
-    unsigned taken = 0;
+}
+
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return (b >> 31) ? ~b : b | 0x80000000u;
+}
+
+// Top-K of one token (one warp) from its logits in shared memory: the K
+// largest sigmoid(L) + bias, ties to the lower expert, NaN as -infinity.
+// Lane k < K returns pick k and its weight.
+__device__ __forceinline__ void few_select(const FewArgs& a, const float* lg, int lane, int& out_e, float& out_w) {
+    uint32_t key[kMaxE / 32];
+    float sc[kMaxE / 32];
+#pragma unroll
+    for (int j = 0; j < kMaxE / 32; ++j) {
+        const int e = lane + 32 * j;
+        key[j] = 0;  // below every key: -infinity is 0x007fffff
+        sc[j] = 0.f;
+        if (e < a.E) {
+            sc[j] = 1.0f / (1.0f + expf(-lg[e]));
+            const float k = sc[j] + __ldg(a.rb + e);
+            key[j] = ordered(isnan(k) ? -INFINITY : k + 0.0f);  // + 0: -0 compares as 0
+        }
+    }
     int my_e = -1;
     float my_s = 0.f, ssum = 0.f;
     for (int k = 0; k < a.K; ++k) {
-        float bk = -INFINITY;
-        int be = 0x7fffffff;
-        for (int j = 0; j < kMaxE / 32; ++j) {
-            const int e = lane + 32 * j;
-            if (e < a.E && !((taken >> j) & 1u) && (s_key[e] > bk || (s_key[e] == bk && e < be))) { bk = s_key[e]; be = e; }
+        uint32_t best = 0;
+#pragma unroll
+        for (int j = 0; j < kMaxE / 32; ++j) best = max(best, key[j]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        int e = 0x7fffffff;
+        float s = 0.f;
+#pragma unroll
+        for (int j = kMaxE / 32 - 1; j >= 0; --j)
+            if (key[j] == best && lane + 32 * j < a.E) {
+                e = lane + 32 * j;
+                s = sc[j];
+            }
+        const int be = (int)__reduce_min_sync(0xffffffffu, (unsigned)e);
+        s = __shfl_sync(0xffffffffu, s, be & 31);
+#pragma unroll
+        for (int j = 0; j < kMaxE / 32; ++j)
+            if (lane + 32 * j == be) key[j] = 0;
+        if (lane == k) {
+            my_e = be;
+            my_s = s;
         }
-        for (int o = 16; o > 0; o >>= 1) {
-            const float ok = __shfl_xor_sync(0xffffffffu, bk, o);
-            const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-            if (ok > bk || (ok == bk && oe < be)) { bk = ok; be = oe; }
-        }
-        if ((be & 31) == lane) taken |= 1u << (be >> 5);
-        if (lane == k) { my_e = be; my_s = s_score[be]; }
-        ssum += s_score[be];
+        ssum += s;
     }
-    int oe;
-    float ow;
-    topp_picks(a.K, a.topp, a.scale, lane, my_e, my_s, ssum, oe, ow);
-    if (lane < a.K) {
-        const size_t o = (size_t)t * a.K + lane;
-        a.idx[o] = oe;
-        a.wts[o] = ow;
-        if (a.topk_idx_out) a.topk_idx_out[o] = oe;
-        if (a.topk_w_out) a.topk_w_out[o] = ow;
-    }
+    topp_picks(a.K, a.topp, a.scale, lane, my_e, my_s, ssum, out_e, out_w);
 }
 
-// sum_k v[k] c[k] s[k / group] over one weight row (one warp): lane l takes
-// the words (eight codes) l, l + 32, ...
-template <typename V>
-__device__ __forceinline__ float few_row(const uint8_t* w, const void* s, size_t s0, int gshift, int stype, int n, V v) {
-    const int lane = threadIdx.x & 31;
-    float acc = 0.f;
-    for (int i = lane; i < n / 8; i += 32) {
-        const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(w) + i);
-        float p = 0.f;
-        for (int j = 0; j < 8; ++j) p = fmaf((float)((int)(c << (28 - 4 * j)) >> 28), v(8 * i + j), p);
-        acc = fmaf(load_scale(s, s0 + ((8 * i) >> gshift), stype), p, acc);
-    }
-    return few_sum(acc);
-}
+template <int NT, bool kCoarse>
+__global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) {
+    namespace cg = cooperative_groups;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ FewPicks P;
+    __shared__ float s_logit[kFewTok][kMaxE];
+    __shared__ int s_e[kFewMaxU];
+    __shared__ float s_w[kFewMaxU];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, q = lane & 3;
+    const int T = a.T, H = a.H, half = H / 2;
+    const int chunks = (H + kChunkK - 1) / kChunkK;
+    const int xs_bytes = x_stride<kCoarse>(chunks);
+    constexpr int kRed = kFewWarps * 4 * NT * 16;
+    float* red = reinterpret_cast<float*>(smem + kFewWarps * kFewDepth * kStageBytes);  // [2][warp][4 NT][16]
+    float* xs = red + 2 * kRed;                                                         // [chunks][4 NT]
+    int8_t* xq = reinterpret_cast<int8_t*>(xs + chunks * 4 * NT);                       // [token][part][xs_bytes]
+    const uint32_t ring = smem_addr(smem + warp * (kFewDepth * kStageBytes));
 
-// h of one pick (or of the shared expert, blockIdx.y = K) of token blockIdx.z: a warp per element.
-__global__ void __launch_bounds__(256) few_gate_up_kernel(FewArgs a) {
-    const int t = blockIdx.z, k = blockIdx.y, lane = threadIdx.x & 31;
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    // Tile i of the layer: 32 h elements, the shared expert's first.  A CTA
+    // takes tiles blockIdx.x + k gridDim.x; of a tile, warp (j, sub) = (warp /
+    // 4, warp % 4) takes the chunks j, j + 4, ... of gate rows 8 sub .. + 7
+    // and the same up rows: mma rows g and g + 8 of a lane are one h element.
+    const int sub = warp & 3, j = warp >> 2;
+    const int per = j < chunks ? (chunks - j - 1) / 4 + 1 : 0;
+    const int shared_tiles = a.Is / kFewTileRows, expert_tiles = a.I / kFewTileRows;
+    int known = shared_tiles;  // tiles whose expert is known
+    struct Tile {
+        const uint8_t* w;
+        const void* s;
+        size_t row;  // this warp's first gate row in the matrix
+        int I, u, i0;
+    };
+    auto tile = [&](int i) {
+        Tile t;
+        if (i < shared_tiles) {
+            t.u = -1;
+            t.i0 = i * kFewTileRows;
+            t.I = a.Is;
+            t.w = a.sh_w13;
+            t.s = a.sh_s13;
+            t.row = t.i0 + 8 * sub;
+        } else {
+            t.u = (i - shared_tiles) / expert_tiles;
+            t.i0 = (i - shared_tiles - t.u * expert_tiles) * kFewTileRows;
+            t.I = a.I;
+            t.w = a.w13;
+            t.s = a.s13;
+            t.row = (size_t)P.expert[t.u] * 2 * a.I + t.i0 + 8 * sub;
+        }
+        return t;
+    };
+    int it = blockIdx.x, ic = j, islot = 0, off[4] = {}, ahead = 0;  // next copy; stages in flight or unread
+    const uint8_t* ip = nullptr;
+    auto open_tile = [&]() {
+        if (it >= known) return;
+        const Tile t = tile(it);
+        ip = t.w + t.row * half + (lane & 7) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (lane >> 3) + 4 * i;
+            off[i] = (r < 8 ? r : t.I + r - 8) * half;
+        }
+    };
+    auto issue = [&]() {
+        if (it < known && per > 0) {
+            issue_chunk(ring + islot * kStageBytes, ip + ic * (kChunkK / 2), off, ic * kChunkK + (lane & 7) * 32 < H, lane);
+            islot = islot == kFewDepth - 1 ? 0 : islot + 1;
+            ++ahead;
+            ic += 4;
+            if (ic >= chunks) {
+                ic = j;
+                it += gridDim.x;
+                open_tile();
+            }
+        }
+        cp_async_commit();
+    };
+    open_tile();
+    for (int i = 0; i < kFewDepth; ++i) issue();
+
     pdl_wait();
     pdl_release();
-    const bool sh = k == a.K;
-    const int I = sh ? a.Is : a.I, e = sh ? 0 : a.idx[(size_t)t * a.K + k];
-    if (i >= I || e < 0) return;
-    const uint8_t* w = sh ? a.sh_w13 : a.w13 + (size_t)e * 2 * I * (a.H / 2);
-    const void* s = sh ? a.sh_s13 : a.s13;
-    const size_t r0 = sh ? 0 : (size_t)e * 2 * I;
-    const __nv_bfloat16* x = a.x + (size_t)t * a.H;
-    auto v = [&](int h) { return __bfloat162float(x[h]); };
-    const float g = few_row(w + (size_t)i * (a.H / 2), s, (r0 + i) * a.G13, a.gshift, a.stype, a.H, v);
-    const float u = few_row(w + (size_t)(I + i) * (a.H / 2), s, (r0 + I + i) * a.G13, a.gshift, a.stype, a.H, v);
-    if (lane == 0) {
-        float* h = sh ? a.h + (size_t)a.T * a.K * a.I + (size_t)t * I : a.h + ((size_t)t * a.K + k) * I;
-        h[i] = silu_mul(g, u);
+
+    // Router logits of this CTA's experts, to every CTA of the cluster.
+    {
+        const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+        const int epc = (a.E + size - 1) / size, e_hi = min(a.E, (rank + 1) * epc);
+        auto put = [&](int t, int e, float v) {
+            for (int r = 0; r < size; ++r) *cluster.map_shared_rank(&s_logit[t][e], r) = v;
+        };
+        if (size > 1) cluster.sync();  // every CTA of the cluster has started
+        if (a.lslices > 0) {
+            for (int i = tid; i < T * (e_hi - rank * epc); i += kFewThreads) {
+                const int t = i / (e_hi - rank * epc), e = rank * epc + i % (e_hi - rank * epc);
+                float v = 0.f;
+                for (int s = 0; s < a.lslices; ++s) v += __ldcg(a.lpart + ((size_t)s * T + t) * a.E + e);
+                put(t, e, v);
+            }
+        } else {
+            for (int e = rank * epc + warp; e < e_hi; e += kFewWarps) {
+                float acc[kFewTok] = {};
+                const float4* w = reinterpret_cast<const float4*>(a.rw + (size_t)e * H) + lane;
+                const uint2* x = reinterpret_cast<const uint2*>(a.x) + lane;
+                for (int b = 0; b < H / 128; b += 4) {
+                    float4 wv[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        wv[i] = b + i < H / 128 ? __ldg(w + (b + i) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int t = 0; t < kFewTok; ++t) {
+                        if (t >= T) break;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (b + i >= H / 128) break;
+                            const uint2 xv = __ldg(x + (size_t)t * (H / 4) + (b + i) * 32);
+                            acc[t] = fmaf(bf16lo(xv.x), wv[i].x, acc[t]);
+                            acc[t] = fmaf(bf16hi(xv.x), wv[i].y, acc[t]);
+                            acc[t] = fmaf(bf16lo(xv.y), wv[i].z, acc[t]);
+                            acc[t] = fmaf(bf16hi(xv.y), wv[i].w, acc[t]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < kFewTok; ++t) {
+                    if (t >= T) break;
+                    float v = acc[t];
+                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                    if (lane < size) *cluster.map_shared_rank(&s_logit[t][e], lane) = v;
+                }
+            }
+        }
+    }
+
+    // int8 activations, while the cluster's other logits arrive
+    for (int t = 0, c = warp; t < T;) {
+        if (c >= chunks) {
+            c -= chunks;
+            ++t;
+            continue;
+        }
+        const int k = c * kChunkK + 8 * lane;
+        const uint4 v = k < H ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * H + k)) : make_uint4(0, 0, 0, 0);
+        int8_t* r = xq + 2 * t * xs_bytes + c * kChunkK;
+        quantize_chunk<kCoarse>(v, r, r + xs_bytes, xs + c * 4 * NT + t, lane);
+        c += kFewWarps;
+    }
+    if (cluster.num_blocks() > 1) cluster.sync();
+    else __syncthreads();
+
+    if (warp < T) {
+        int e;
+        float w;
+        few_select(a, s_logit[warp], lane, e, w);
+        if (lane < a.K) {
+            const int i = warp * a.K + lane;
+            s_e[i] = e;
+            s_w[i] = w;
+            if (blockIdx.x == 0) {
+                a.idx[i] = e;
+                if (a.topk_idx_out) a.topk_idx_out[i] = e;
+                if (a.topk_w_out) a.topk_w_out[i] = w;
+            }
+        }
+    }
+    __syncthreads();
+    few_gather(P, T, a.K, tid < T * a.K ? s_e[tid] : -1, tid < T * a.K ? s_w[tid] : 0.f);
+    {  // the routed tiles are known now: fill the ring
+        const bool was = it < known;
+        known = shared_tiles + P.U * expert_tiles;
+        if (!was) open_tile();
+        // As many groups again as the first ones held no copy: the group of the
+        // n-th stage is then never among the last kFewDepth - 1 when it is read.
+        for (int i = ahead; i < kFewDepth; ++i) issue();
+    }
+
+    uint32_t xrow[NT];
+    const float* xsc[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int t = min(4 * n + (g >> 1), T - 1);
+        xrow[n] = smem_addr(xq + (2 * t + (g & 1)) * xs_bytes);
+        xsc[n] = xs + min(4 * n + q, T - 1);
+    }
+    int slot = 0, parity = 0;
+    for (int i = blockIdx.x; i < known; i += gridDim.x, parity ^= 1) {
+        const Tile t = tile(i);
+        const size_t s0 = (t.row + g) * a.G13, s8 = (t.row + t.I + g) * a.G13;
+        const unsigned tokens = t.u < 0 ? 0xffu : P.tokens[t.u];
+        float acc[NT][2] = {};
+        float nxt[4];
+        if (per > 0) load_chunk_scales<kCoarse>(nxt, t.s, s0, s8, j, a.gshift, a.G13, a.stype, q);
+        for (int c = j; c < chunks; c += 4) {
+            float sc[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sc[u] = nxt[u];
+            if (c + 4 < chunks) load_chunk_scales<kCoarse>(nxt, t.s, s0, s8, c + 4, a.gshift, a.G13, a.stype, q);
+            cp_async_wait<kFewDepth - 1>();
+            __syncwarp();
+            const uint32_t st = ring + slot * kStageBytes;
+            slot = slot == kFewDepth - 1 ? 0 : slot + 1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (NT > 1 && !((tokens >> (4 * n)) & 15u)) continue;
+                const uint32_t xb[1] = {xrow[n] + c * kChunkK};
+                float p[1][2];
+                chunk_mma<1, kCoarse>(st, xb, sc, a.gshift, lane, p);
+                const float s = xsc[n][c * 4 * NT];
+                acc[n][0] = fmaf(p[0][0], s, acc[n][0]);
+                acc[n][1] = fmaf(p[0][1], s, acc[n][1]);
+            }
+            __syncwarp();
+            issue();
+        }
+        float* part = red + parity * kRed;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float* o = part + (warp * 4 * NT + 4 * n + q) * 16;
+            o[g] = acc[n][0];
+            o[g + 8] = acc[n][1];
+        }
+        __syncthreads();
+        if (warp < T && ((tokens >> warp) & 1u)) {  // a warp per token, a lane per h element
+            float gv = 0.f, uv = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* o = part + ((k * 4 + (lane >> 3)) * 4 * NT + warp) * 16 + (lane & 7);
+                gv += o[0];
+                uv += o[8];
+            }
+            float h = silu_mul(gv, uv);
+            if (t.u >= 0) h *= P.weight[t.u][warp];
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
+            // block_scale of the magnitude rounded up to bf16's seven bits
+            float s, inv;
+            block_scale((m >> 16) + ((m & 0xffffu) != 0), &s, &inv);
+            const uint32_t f = fixed16(h, inv);
+            const int at = t.i0 + (lane & ~7) + ((lane & 1) << 2) + ((lane & 7) >> 1);  // order of lo8 / hi8
+            const size_t base = t.u < 0 ? (size_t)T * a.K * 2 * a.I + (size_t)warp * 2 * a.Is
+                                        : (size_t)P.slot[t.u][warp] * 2 * a.I;
+            a.hq[base + at] = (int8_t)((f + 128) >> 8);
+            a.hq[base + t.I + at] = (int8_t)f;
+            if (lane == 0)
+                a.hs[t.u < 0 ? (T * a.K * a.I + warp * a.Is + t.i0) / 32 : (P.slot[t.u][warp] * a.I + t.i0) / 32] = s * 0x1p-12f;
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// One staged chunk of w2 times one tile of four tokens, block by block of 32
+// columns, each with the token's own scale hv[b] beside the row's.
+template <bool kCoarse>
+__device__ __forceinline__ void down_mma(uint32_t stage, const uint2 (&x)[8], const float (&hv)[8], const float (&sc)[4],
+                                         int gshift, int lane, float (&t)[2]) {
+    const int g = lane >> 2, q = lane & 3, quad = lane & 28;
+    const uint32_t row = stage + g * 128 + (seg_perm(g) << 4);
+    t[0] = t[1] = 0.f;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        const uint32_t at = (row ^ (b << 4)) + q * 4;
+        const uint32_t wa = lds32(at), wb = lds32(at + 1024);
+        const uint32_t a[4] = {lo8(wa), lo8(wb), hi8(wa), hi8(wb)};
+        int d[4];
+        mma_s8_first(d, a, x[b].x, x[b].y);
+        const bool fine = !kCoarse && gshift == 5;
+        const int from = quad | (kCoarse ? b >> 2 : fine ? b & 3 : b >> 1);
+        const float s0 = __shfl_sync(0xffffffffu, fine ? sc[b >> 2] : sc[0], from);
+        const float s8 = __shfl_sync(0xffffffffu, fine ? sc[2 + (b >> 2)] : sc[2], from);
+        t[0] = fmaf((float)(d[0] * 256 + d[1]), s0 * hv[b], t[0]);
+        t[1] = fmaf((float)(d[2] * 256 + d[3]), s8 * hv[b], t[1]);
     }
 }
 
-// One output element: a warp.
-__global__ void __launch_bounds__(256) few_down_kernel(FewArgs a) {
-    const int t = blockIdx.y, lane = threadIdx.x & 31;
-    const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
+// Down projection of whole output tiles: 16 rows, the shared expert and all
+// touched ones as one long sum, its chunks dealt out to the CTA's warps.
+template <int NT, bool kCoarse>
+__global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ FewPicks P;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, q = lane & 3;
+    const int T = a.T;
+    constexpr int kRed = kFewWarps * 4 * NT * 16;
+    float* red = reinterpret_cast<float*>(smem + kFewWarps * kFewDepth * kStageBytes);  // [2][warp][4 NT][16]
+    const uint32_t ring = smem_addr(smem + warp * (kFewDepth * kStageBytes));
+    const int Cs = (a.Is + kChunkK - 1) / kChunkK, Ci = (a.I + kChunkK - 1) / kChunkK;
+    const int tiles = a.H / 16;
+    int units = Cs;  // (expert, chunk) pairs of a tile, as far as they are known: the shared expert's first
+    bool all = false;
+
+    int it = blockIdx.x, iv = warp, islot = 0, ahead = 0;  // next copy; stages filled before the picks are known
+    auto issue = [&]() {
+        if (it < tiles && iv < units) {
+            const bool sh = iv < Cs;
+            const int u = sh ? 0 : (iv - Cs) / Ci, c = sh ? iv : iv - Cs - u * Ci, I = sh ? a.Is : a.I;
+            const uint8_t* w = (sh ? a.sh_w2 : a.w2 + (size_t)P.expert[u] * a.H * (I / 2)) + (size_t)it * 16 * (I / 2) +
+                               c * (kChunkK / 2) + (lane & 7) * 16;
+            int off[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) off[i] = ((lane >> 3) + 4 * i) * (I / 2);
+            issue_chunk(ring + islot * kStageBytes, w, off, c * kChunkK + (lane & 7) * 32 < I, lane);
+            islot = islot == kFewDepth - 1 ? 0 : islot + 1;
+            ++ahead;
+            iv += kFewWarps;
+            if (all && iv >= units) {
+                iv = warp;
+                it += gridDim.x;
+            }
+        }
+        cp_async_commit();
+    };
+    for (int i = 0; i < kFewDepth; ++i) issue();
+
     pdl_wait();
     pdl_release();
-    if (j >= a.H) return;
-    float y = 0.f;
-    for (int k = 0; k < a.K; ++k) {
-        const int e = a.idx[(size_t)t * a.K + k];
-        if (e < 0) continue;
-        const float* h = a.h + ((size_t)t * a.K + k) * a.I;
-        const size_t r = (size_t)e * a.H + j;
-        y = fmaf(a.wts[(size_t)t * a.K + k],
-                 few_row(a.w2 + r * (a.I / 2), a.s2, r * a.G2, a.gshift, a.stype, a.I, [&](int i) { return h[i]; }), y);
+    few_gather(P, T, a.K, tid < T * a.K ? __ldcg(a.idx + tid) : -1, 0.f);
+    units = Cs + P.U * Ci;
+    all = true;
+    if (iv >= units && warp < units) {
+        iv = warp;
+        it += gridDim.x;
     }
-    if (a.Is > 0) {
-        const float* h = a.h + (size_t)a.T * a.K * a.I + (size_t)t * a.Is;
-        y += few_row(a.sh_w2 + (size_t)j * (a.Is / 2), a.sh_s2, (size_t)j * a.Gs2, a.gshift, a.stype, a.Is,
-                     [&](int i) { return h[i]; });
+    for (int i = ahead; i < kFewDepth; ++i) issue();  // see few_gate_up_kernel
+
+    const size_t hq_shared = (size_t)T * a.K * 2 * a.I;
+    const int hs_shared = T * a.K * a.I;
+    int slot = 0, parity = 0;
+    for (int i = blockIdx.x; i < tiles; i += gridDim.x, parity ^= 1) {
+        float acc[NT][2] = {};
+        for (int v = warp; v < units; v += kFewWarps) {
+            const bool sh = v < Cs;
+            const int u = sh ? 0 : (v - Cs) / Ci, c = sh ? v : v - Cs - u * Ci, I = sh ? a.Is : a.I;
+            const size_t row = (sh ? 0 : (size_t)P.expert[u] * a.H) + (size_t)i * 16;
+            const int G = sh ? a.Gs2 : a.G2;
+            float sc[4];
+            load_chunk_scales<kCoarse>(sc, sh ? a.sh_s2 : a.s2, (row + g) * G, (row + g + 8) * G, c, a.gshift, G, a.stype, q);
+            const int blocks = min(8, (I - c * kChunkK) / 32);  // 4 or 8
+            const unsigned tokens = sh ? 0xffu : P.tokens[u];
+            bool waited = false;
+            const uint32_t st = ring + slot * kStageBytes;
+            slot = slot == kFewDepth - 1 ? 0 : slot + 1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (NT > 1 && !((tokens >> (4 * n)) & 15u)) continue;
+                // this lane's B row (token tb, part g % 2) and the scales of its D column (token td)
+                const int tb = 4 * n + (g >> 1), td = 4 * n + q;
+                const int sb = sh ? (tb < T ? tb : -1) : P.slot[u][tb], sd = sh ? (td < T ? td : -1) : P.slot[u][td];
+                uint2 x[8];
+                float hv[8];
+                const uint2* xp = reinterpret_cast<const uint2*>(a.hq + (sh ? hq_shared : 0) +
+                                                                 (size_t)(2 * max(sb, 0) + (g & 1)) * I + c * kChunkK) + q;
+                const float4* hp = reinterpret_cast<const float4*>(a.hs + ((sh ? hs_shared : 0) + max(sd, 0) * I + c * kChunkK) / 32);
+#pragma unroll
+                for (int b = 0; b < 8; ++b) x[b] = sb >= 0 && b < blocks ? __ldcg(xp + 4 * b) : make_uint2(0, 0);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float4 f = sd >= 0 && 4 * b < blocks ? __ldcg(hp + b) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    hv[4 * b] = f.x;
+                    hv[4 * b + 1] = f.y;
+                    hv[4 * b + 2] = f.z;
+                    hv[4 * b + 3] = f.w;
+                }
+                if (!waited) {
+                    cp_async_wait<kFewDepth - 1>();
+                    __syncwarp();
+                    waited = true;
+                }
+                float t[2];
+                down_mma<kCoarse>(st, x, hv, sc, a.gshift, lane, t);
+                if (sd >= 0) {
+                    acc[n][0] += t[0];
+                    acc[n][1] += t[1];
+                }
+            }
+            __syncwarp();
+            issue();
+        }
+        float* part = red + parity * kRed;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float* o = part + (warp * 4 * NT + 4 * n + q) * 16;
+            o[g] = acc[n][0];
+            o[g + 8] = acc[n][1];
+        }
+        __syncthreads();
+        if (tid < 16 * T) {
+            const int r = tid & 15, t = tid >> 4;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFewWarps; ++w) v += part[(w * 4 * NT + t) * 16 + r];
+            const size_t o = (size_t)t * a.H + i * 16 + r;
+            if (a.flags & kFlagResidual) v += __bfloat162float(a.x[o]);
+            if (a.flags & kFlagOutF32) static_cast<float*>(a.out)[o] = v;
+            else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+        }
     }
-    if (lane) return;
-    const size_t o = (size_t)t * a.H + j;
-    if (a.flags & kFlagResidual) y += __bfloat162float(a.x[o]);
-    if (a.flags & kFlagOutF32) static_cast<float*>(a.out)[o] = y;
-    else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
+    cp_async_wait<0>();
 }
 
-int few_pass_tokens(const FewArgs&) { return 8; }
-int few_pass_launches(const FewArgs&) { return 3; }
+namespace {
+
+template <int NT>
+size_t few_smem_base() {
+    return (size_t)kFewWarps * kFewDepth * kStageBytes + 2 * (size_t)kFewWarps * 4 * NT * 16 * 4;
+}
+
+// SMs of the current device, and the CTAs of the gate/up kernel that run at
+// once in clusters of kFewCluster.
+struct FewDevice {
+    int sms, clustered;
+};
+
+cudaError_t few_launch_cluster(void (*k)(FewArgs), int grid, int cluster, size_t smem, cudaStream_t stream, const FewArgs& a,
+                               int* max_clusters) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(kFewThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = cluster > 1 ? 2 : 1;
+    if (max_clusters) {
+        c.attrs = at + 1;
+        c.numAttrs = 1;
+        return cudaOccupancyMaxActiveClusters(max_clusters, k, &c);
+    }
+    return cudaLaunchKernelEx(&c, k, a);
+}
+
+template <int NT, bool kCoarse>
+cudaError_t few_launch(const FewArgs& a, cudaStream_t stream) {
+    auto* up = few_gate_up_kernel<NT, kCoarse>;
+    auto* down = few_down_kernel<NT, kCoarse>;
+    static FewDevice devs[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    FewDevice& d = devs[dev];
+    if (d.clustered == 0) {
+        int n = 0, sms = 0;
+        // static shared memory comes on top of the dynamic part
+        constexpr int kMax = kFewSmemMax - 12 * 1024;
+        e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
+        if (e == cudaSuccess) e = few_launch_cluster(up, kFewCluster, kFewCluster, kMax, nullptr, a, &n);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        d.sms = sms;
+        d.clustered = n * kFewCluster;
+    }
+    const int chunks = (a.H + kChunkK - 1) / kChunkK;
+    const size_t smem = few_smem_base<NT>() + (size_t)chunks * 4 * NT * 4 + (size_t)2 * a.T * x_stride<kCoarse>(chunks);
+    const int cluster = a.lslices > 0 ? 1 : kFewCluster, most = a.lslices > 0 ? d.sms : d.clustered;
+    const int touched = a.E < a.T * a.K ? a.E : a.T * a.K;
+    const int tiles = a.Is / kFewTileRows + touched * (a.I / kFewTileRows);
+    int grid = (tiles + cluster - 1) / cluster * cluster;
+    if (grid > most) grid = most;
+    e = few_launch_cluster(up, grid, cluster, smem, stream, a, nullptr);
+    const int out_tiles = a.H / 16;
+    if (e == cudaSuccess)
+        e = launch_pdl(down, dim3(out_tiles < d.sms ? out_tiles : d.sms), dim3(kFewThreads), few_smem_base<NT>(), stream, a);
+    return e;
+}
+
+}  // namespace
+
+int few_pass_tokens(const FewArgs& a) {
+    const int fit = kFewXMax / (2 * x_stride<true>((a.H + kChunkK - 1) / kChunkK));
+    return fit < kFewTok ? fit : kFewTok;
+}
+
+int few_pass_launches(const FewArgs& a) { return few_split_router(a.E, a.H) ? 3 : 2; }
 
 size_t few_workspace(FewArgs& a, void* ws) {
     size_t o = 0;
@@ -133,20 +622,31 @@ size_t few_workspace(FewArgs& a, void* ws) {
         o = (o + bytes + 255) & ~size_t(255);
         return p;
     };
-    const size_t TK = (size_t)a.T * a.K;
+    const size_t TK = (size_t)a.T * a.K, n = TK * a.I + (size_t)a.T * a.Is;
     a.idx = reinterpret_cast<int32_t*>(take(TK * 4));
-    a.wts = reinterpret_cast<float*>(take(TK * 4));
-    a.h = reinterpret_cast<float*>(take((TK * a.I + (size_t)a.T * a.Is) * 4));
+    a.hq = reinterpret_cast<int8_t*>(take(2 * n));
+    a.hs = reinterpret_cast<float*>(take(n / 32 * 4));
+    a.lslices = few_split_router(a.E, a.H) ? few_logit_slices(a.H) : 0;
+    a.lpart = reinterpret_cast<float*>(take((size_t)a.lslices * a.T * a.E * 4));
     return o;
 }
 
 cudaError_t launch_few(const FewArgs& a, cudaStream_t stream) {
-    cudaError_t e = launch_pdl(few_route_kernel, dim3(a.T), dim3(256), 0, stream, a);
-    const int im = a.Is > a.I ? a.Is : a.I;
-    if (e == cudaSuccess)
-        e = launch_pdl(few_gate_up_kernel, dim3((im + 7) / 8, a.K + (a.Is > 0), a.T), dim3(256), 0, stream, a);
-    if (e == cudaSuccess) e = launch_pdl(few_down_kernel, dim3((a.H + 7) / 8, a.T), dim3(256), 0, stream, a);
-    return e;
+    if (a.lslices > 0) {
+        Params p = {};
+        p.T = a.T;
+        p.H = a.H;
+        p.E = a.E;
+        p.x = a.x;
+        p.rw = a.rw;
+        p.lpart = a.lpart;
+        p.lslices = a.lslices;
+        const cudaError_t e = launch_router_logits(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    const bool coarse = a.gshift >= 7;
+    if (a.T <= 4) return coarse ? few_launch<1, true>(a, stream) : few_launch<1, false>(a, stream);
+    return coarse ? few_launch<2, true>(a, stream) : few_launch<2, false>(a, stream);
 }
 
 }  // namespace moe

@@ -42,9 +42,11 @@ struct FewArgs {
     int gshift, stype;
     int G13, G2, Gs2;  // scales per row of w13 (and sh_w13), w2, sh_w2
     // workspace
-    int32_t* idx;  // [T][K]
-    float* wts;    // [T][K]
-    float* h;      // [T*K][I] then [T][Is]: the SwiGLU intermediate
+    int32_t* idx;  // [T][K] picks (-1: dropped)
+    int8_t* hq;    // [T*K][2][I] then [T][2][Is]: both int8 parts of h
+    float* hs;     // [T*K][I/32] then [T][Is/32]: their scales
+    float* lpart;  // [lslices][T][E] partial router logits (lslices = 0: none)
+    int lslices;
 };
 
 // One scale, as f32.

@@ -12,6 +12,9 @@ cudaError_t launch_router(const Params& p, bool small_path, cudaStream_t stream)
 // Hidden-dimension slices of the split small-batch router's partial logits
 // (0: the cluster router computes the logits itself).
 int router_split_slices(int E, int H);
+// Partial router logits over lslices hidden slices (see router_logits_kernel)
+// of p.x and p.rw into p.lpart [lslices][T][E].
+cudaError_t launch_router_logits(const Params& p, cudaStream_t stream);
 // Tensor-core router logits of the large-batch path: the weight split and
 // the logits kernel (slices of the hidden dimension, partials in lpart).
 cudaError_t launch_router_tc(const Params& p, cudaStream_t stream);
