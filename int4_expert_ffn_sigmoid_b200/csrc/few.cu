@@ -186,22 +186,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         }
         return t;
     };
-    int it = blockIdx.x, ic = j, islot = 0, off[4] = {}, ahead = 0;  // next copy; stages in flight or unread
-    const uint8_t* ip = nullptr;
+    int it = blockIdx.x, ic = j, ahead = 0;  // next copy; stages filled before the picks are known
+    uint32_t dst = ring + stage_at(lane);
+    const uint32_t dst_end = dst + kFewDepth * kStageBytes;
+    const uint8_t* ip[4] = {};
     auto open_tile = [&]() {
         if (it >= known) return;
         const Tile t = tile(it);
-        ip = t.w + t.row * half + (lane & 7) * 16;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = (lane >> 3) + 4 * i;
-            off[i] = (r < 8 ? r : t.I + r - 8) * half;
+            ip[i] = t.w + (t.row + (r < 8 ? r : t.I + r - 8)) * half + (lane & 7) * 16;
         }
     };
     auto issue = [&]() {
         if (it < known && per > 0) {
-            issue_chunk(ring + islot * kStageBytes, ip + ic * (kChunkK / 2), off, ic * kChunkK + (lane & 7) * 32 < H, lane);
-            islot = islot == kFewDepth - 1 ? 0 : islot + 1;
+            issue_chunk(dst, ip, ic, ic * kChunkK + (lane & 7) * 32 < H);
+            dst += kStageBytes;
+            if (dst == dst_end) dst -= kFewDepth * kStageBytes;
             ++ahead;
             ic += 4;
             if (ic >= chunks) {
@@ -269,18 +271,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     }
 
     // int8 activations, while the cluster's other logits arrive
-    for (int t = 0, c = warp; t < T;) {
-        if (c >= chunks) {
-            c -= chunks;
-            ++t;
-            continue;
-        }
-        const int k = c * kChunkK + 8 * lane;
-        const uint4 v = k < H ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * H + k)) : make_uint4(0, 0, 0, 0);
-        int8_t* r = xq + 2 * t * xs_bytes + c * kChunkK;
-        quantize_chunk<kCoarse>(v, r, r + xs_bytes, xs + c * 4 * NT + t, lane);
-        c += kFewWarps;
-    }
+    quantize_tokens<kCoarse>(a.x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
     if (cluster.num_blocks() > 1) cluster.sync();
     else __syncthreads();
 
@@ -319,18 +310,26 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         xsc[n] = xs + min(4 * n + q, T - 1);
     }
     int slot = 0, parity = 0;
+    float nxt[4];  // the next chunk's scales, on their way while this one is multiplied
+    ScaleRows sr;
+    auto open_scales = [&](const Tile& t) {
+        sr.open(t.s, t.row + g, t.row + t.I + g, a.G13, a.stype);
+        if (per > 0) load_chunk_scales<kCoarse>(nxt, sr, j, a.gshift, a.G13, a.stype, q);
+    };
+    Tile t;
+    if (blockIdx.x < known) open_scales(t = tile(blockIdx.x));
     for (int i = blockIdx.x; i < known; i += gridDim.x, parity ^= 1) {
-        const Tile t = tile(i);
-        const size_t s0 = (t.row + g) * a.G13, s8 = (t.row + t.I + g) * a.G13;
+        Tile after = t;
+        if (per == 0 && i + (int)gridDim.x < known) after = tile(i + gridDim.x);
         const unsigned tokens = t.u < 0 ? 0xffu : P.tokens[t.u];
         float acc[NT][2] = {};
-        float nxt[4];
-        if (per > 0) load_chunk_scales<kCoarse>(nxt, t.s, s0, s8, j, a.gshift, a.G13, a.stype, q);
         for (int c = j; c < chunks; c += 4) {
             float sc[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) sc[u] = nxt[u];
-            if (c + 4 < chunks) load_chunk_scales<kCoarse>(nxt, t.s, s0, s8, c + 4, a.gshift, a.G13, a.stype, q);
+            scale_values(sc, a.stype);
+            if (c + 4 < chunks) load_chunk_scales<kCoarse>(nxt, sr, c + 4, a.gshift, a.G13, a.stype, q);
+            else if (i + (int)gridDim.x < known) open_scales(after = tile(i + gridDim.x));
             cp_async_wait<kFewDepth - 1>();
             __syncwarp();
             const uint32_t st = ring + slot * kStageBytes;
@@ -379,6 +378,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
             if (lane == 0)
                 a.hs[t.u < 0 ? (T * a.K * a.I + warp * a.Is + t.i0) / 32 : (P.slot[t.u][warp] * a.I + t.i0) / 32] = s * 0x1p-12f;
         }
+        t = after;
     }
     cp_async_wait<0>();
 }
@@ -389,11 +389,11 @@ template <bool kCoarse>
 __device__ __forceinline__ void down_mma(uint32_t stage, const uint2 (&x)[8], const float (&hv)[8], const float (&sc)[4],
                                          int gshift, int lane, float (&t)[2]) {
     const int g = lane >> 2, q = lane & 3, quad = lane & 28;
-    const uint32_t row = stage + g * 128 + (seg_perm(g) << 4);
+    const uint32_t row = stage + g * 128 + (seg_perm(g) << 4) + q * 4;
     t[0] = t[1] = 0.f;
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
-        const uint32_t at = (row ^ (b << 4)) + q * 4;
+        const uint32_t at = row ^ (b << 4);
         const uint32_t wa = lds32(at), wb = lds32(at + 1024);
         const uint32_t a[4] = {lo8(wa), lo8(wb), hi8(wa), hi8(wb)};
         int d[4];
@@ -424,18 +424,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
     int units = Cs;  // (expert, chunk) pairs of a tile, as far as they are known: the shared expert's first
     bool all = false;
 
-    int it = blockIdx.x, iv = warp, islot = 0, ahead = 0;  // next copy; stages filled before the picks are known
+    int it = blockIdx.x, iv = warp, ahead = 0;  // next copy; stages filled before the picks are known
+    uint32_t dst = ring + stage_at(lane);
+    const uint32_t dst_end = dst + kFewDepth * kStageBytes;
     auto issue = [&]() {
         if (it < tiles && iv < units) {
             const bool sh = iv < Cs;
             const int u = sh ? 0 : (iv - Cs) / Ci, c = sh ? iv : iv - Cs - u * Ci, I = sh ? a.Is : a.I;
-            const uint8_t* w = (sh ? a.sh_w2 : a.w2 + (size_t)P.expert[u] * a.H * (I / 2)) + (size_t)it * 16 * (I / 2) +
-                               c * (kChunkK / 2) + (lane & 7) * 16;
-            int off[4];
+            const uint8_t* w = sh ? a.sh_w2 : a.w2 + (size_t)P.expert[u] * a.H * (I / 2);
+            const uint8_t* ip[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) off[i] = ((lane >> 3) + 4 * i) * (I / 2);
-            issue_chunk(ring + islot * kStageBytes, w, off, c * kChunkK + (lane & 7) * 32 < I, lane);
-            islot = islot == kFewDepth - 1 ? 0 : islot + 1;
+            for (int i = 0; i < 4; ++i) ip[i] = w + (size_t)(it * 16 + (lane >> 3) + 4 * i) * (I / 2) + (lane & 7) * 16;
+            issue_chunk(dst, ip, c, c * kChunkK + (lane & 7) * 32 < I);
+            dst += kStageBytes;
+            if (dst == dst_end) dst -= kFewDepth * kStageBytes;
             ++ahead;
             iv += kFewWarps;
             if (all && iv >= units) {
@@ -461,49 +463,89 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
     const size_t hq_shared = (size_t)T * a.K * 2 * a.I;
     const int hs_shared = T * a.K * a.I;
     int slot = 0, parity = 0;
+    // A unit's row scales and its first tile of tokens are loaded one unit ahead.
+    struct Unit {
+        bool sh;
+        int u, c, I, blocks;
+        unsigned tokens;
+    };
+    auto unit = [&](int v) {
+        Unit t;
+        t.sh = v < Cs;
+        t.u = t.sh ? 0 : (v - Cs) / Ci;
+        t.c = t.sh ? v : v - Cs - t.u * Ci;
+        t.I = t.sh ? a.Is : a.I;
+        t.blocks = min(8, (t.I - t.c * kChunkK) / 32);  // 4 or 8
+        t.tokens = t.sh ? (1u << T) - 1 : P.tokens[t.u];
+        return t;
+    };
+    auto load_scales = [&](const Unit& t, int i, float (&sc)[4]) {
+        const size_t row = (t.sh ? 0 : (size_t)P.expert[t.u] * a.H) + (size_t)i * 16;
+        const int G = t.sh ? a.Gs2 : a.G2;
+        ScaleRows sr;
+        sr.open(t.sh ? a.sh_s2 : a.s2, row + g, row + g + 8, G, a.stype);
+        load_chunk_scales<kCoarse>(sc, sr, t.c, a.gshift, G, a.stype, q);
+    };
+    // This lane's B row (token 4 n + g / 2, part g % 2) and the block scales of
+    // its D columns (token 4 n + q); zero for a token that did not pick the expert.
+    auto load_h = [&](const Unit& t, int n, uint2 (&x)[8], float (&hv)[8]) {
+        const int tb = 4 * n + (g >> 1), td = 4 * n + q;
+        const bool hb = (t.tokens >> tb) & 1u, hd = (t.tokens >> td) & 1u;
+        const int sb = t.sh ? tb : P.slot[t.u][tb], sd = t.sh ? td : P.slot[t.u][td];
+        const uint2* xp = reinterpret_cast<const uint2*>(a.hq + (t.sh ? hq_shared : 0) + (size_t)(2 * max(sb, 0) + (g & 1)) * t.I +
+                                                         t.c * kChunkK) + q;
+        const float4* hp = reinterpret_cast<const float4*>(a.hs + ((t.sh ? hs_shared : 0) + max(sd, 0) * t.I + t.c * kChunkK) / 32);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) x[b] = hb && b < t.blocks ? __ldcg(xp + 4 * b) : make_uint2(0, 0);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float4 f = hd && 4 * b < t.blocks ? __ldcg(hp + b) : make_float4(0.f, 0.f, 0.f, 0.f);
+            hv[4 * b] = f.x;
+            hv[4 * b + 1] = f.y;
+            hv[4 * b + 2] = f.z;
+            hv[4 * b + 3] = f.w;
+        }
+    };
+    auto first_n = [&](const Unit& t) { return NT > 1 && !(t.tokens & 15u) ? 1 : 0; };
+    float nsc[4], nhv[8];
+    uint2 nx[8];
+    Unit next;
+    if (warp < units && (int)blockIdx.x < tiles) {
+        next = unit(warp);
+        load_scales(next, blockIdx.x, nsc);
+        load_h(next, first_n(next), nx, nhv);
+    }
     for (int i = blockIdx.x; i < tiles; i += gridDim.x, parity ^= 1) {
         float acc[NT][2] = {};
         for (int v = warp; v < units; v += kFewWarps) {
-            const bool sh = v < Cs;
-            const int u = sh ? 0 : (v - Cs) / Ci, c = sh ? v : v - Cs - u * Ci, I = sh ? a.Is : a.I;
-            const size_t row = (sh ? 0 : (size_t)P.expert[u] * a.H) + (size_t)i * 16;
-            const int G = sh ? a.Gs2 : a.G2;
-            float sc[4];
-            load_chunk_scales<kCoarse>(sc, sh ? a.sh_s2 : a.s2, (row + g) * G, (row + g + 8) * G, c, a.gshift, G, a.stype, q);
-            const int blocks = min(8, (I - c * kChunkK) / 32);  // 4 or 8
-            const unsigned tokens = sh ? 0xffu : P.tokens[u];
-            bool waited = false;
+            const Unit now = next;
+            float sc[4], hv[8];
+            uint2 x[8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sc[u] = nsc[u];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                hv[u] = nhv[u];
+                x[u] = nx[u];
+            }
+            const bool more = v + kFewWarps < units;
+            if (more || i + (int)gridDim.x < tiles) {
+                next = unit(more ? v + kFewWarps : warp);
+                load_scales(next, more ? i : i + gridDim.x, nsc);
+                load_h(next, first_n(next), nx, nhv);
+            }
+            scale_values(sc, a.stype);
+            cp_async_wait<kFewDepth - 1>();
+            __syncwarp();
             const uint32_t st = ring + slot * kStageBytes;
             slot = slot == kFewDepth - 1 ? 0 : slot + 1;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if (NT > 1 && !((tokens >> (4 * n)) & 15u)) continue;
-                // this lane's B row (token tb, part g % 2) and the scales of its D column (token td)
-                const int tb = 4 * n + (g >> 1), td = 4 * n + q;
-                const int sb = sh ? (tb < T ? tb : -1) : P.slot[u][tb], sd = sh ? (td < T ? td : -1) : P.slot[u][td];
-                uint2 x[8];
-                float hv[8];
-                const uint2* xp = reinterpret_cast<const uint2*>(a.hq + (sh ? hq_shared : 0) +
-                                                                 (size_t)(2 * max(sb, 0) + (g & 1)) * I + c * kChunkK) + q;
-                const float4* hp = reinterpret_cast<const float4*>(a.hs + ((sh ? hs_shared : 0) + max(sd, 0) * I + c * kChunkK) / 32);
-#pragma unroll
-                for (int b = 0; b < 8; ++b) x[b] = sb >= 0 && b < blocks ? __ldcg(xp + 4 * b) : make_uint2(0, 0);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float4 f = sd >= 0 && 4 * b < blocks ? __ldcg(hp + b) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    hv[4 * b] = f.x;
-                    hv[4 * b + 1] = f.y;
-                    hv[4 * b + 2] = f.z;
-                    hv[4 * b + 3] = f.w;
-                }
-                if (!waited) {
-                    cp_async_wait<kFewDepth - 1>();
-                    __syncwarp();
-                    waited = true;
-                }
+                if (NT > 1 && !((now.tokens >> (4 * n)) & 15u)) continue;
+                if (NT > 1 && n != first_n(now)) load_h(now, n, x, hv);
                 float t[2];
                 down_mma<kCoarse>(st, x, hv, sc, a.gshift, lane, t);
-                if (sd >= 0) {
+                if ((now.tokens >> (4 * n + q)) & 1u) {
                     acc[n][0] += t[0];
                     acc[n][1] += t[1];
                 }

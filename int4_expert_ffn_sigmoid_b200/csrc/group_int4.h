@@ -49,12 +49,6 @@ struct FewArgs {
     int lslices;
 };
 
-// One scale, as f32.
-__device__ __forceinline__ float load_scale(const void* s, size_t i, int stype) {
-    if (stype == kScaleF32) return __ldg(static_cast<const float*>(s) + i);
-    const unsigned short b = __ldg(static_cast<const unsigned short*>(s) + i);
-    return stype == kScaleBf16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
-}
 
 int linear_launches(const LinearArgs& a);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);

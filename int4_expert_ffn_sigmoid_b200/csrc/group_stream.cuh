@@ -103,42 +103,99 @@ __device__ __forceinline__ void quantize_chunk(uint4 v, int8_t* q0, int8_t* q1, 
     if (lane == 0) *xs = s * 0x1p-12f;
 }
 
-// Issues the copies of a chunk of 16 rows into a stage (one warp).  Lane l
-// copies segment l % 8 of rows l / 8 + 4 i, i < 4, from p + off[i] (p: the
-// segment's place in the first row); `in`: the segment is inside the row.
-// Segments past a row's end are left as they are: their activations are zero,
-// and the sums are of integers.
-__device__ __forceinline__ void issue_chunk(uint32_t stage, const uint8_t* p, const int (&off)[4], bool in, int lane) {
+// All chunks of nt tokens (x: the first token's row, ldx elements apart, K
+// columns) over the CTA's nw warps, four loads in flight a warp; token t's
+// scale of chunk c goes to xs[c * xs_tok + t].
+template <bool kCoarse>
+__device__ __forceinline__ void quantize_tokens(const __nv_bfloat16* x, long long ldx, int K, int chunks, int nt,
+                                                int8_t* xq, int xs_bytes, float* xs, int xs_tok, int warp, int nw,
+                                                int lane) {
+    constexpr int kAhead = 4;
+    for (int i0 = warp; i0 < nt * chunks; i0 += kAhead * nw) {
+        uint4 v[kAhead];
+        int t[kAhead], c[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * nw;
+            t[u] = i / chunks;
+            c[u] = i - t[u] * chunks;
+            const int k = c[u] * kChunkK + 8 * lane;
+            v[u] = t[u] < nt && k < K ? __ldg(reinterpret_cast<const uint4*>(x + t[u] * ldx + k)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (t[u] >= nt) break;
+            int8_t* r = xq + 2 * t[u] * xs_bytes + c[u] * kChunkK;
+            quantize_chunk<kCoarse>(v[u], r, r + xs_bytes, xs + c[u] * xs_tok + t[u], lane);
+        }
+    }
+}
+
+// Where lane l's copies of a chunk go: it copies segment l % 8 of rows l / 8 +
+// 4 i, i < 4, to stage_at(l) ^ (i odd ? 32 : 0) + 512 i.
+__device__ __forceinline__ uint32_t stage_at(int lane) {
+    const int r = lane >> 3;
+    return r * 128 + (((lane & 7) ^ seg_perm(r)) << 4);
+}
+
+// Issues the copies of a chunk of 16 rows (one warp).  dst: the stage's
+// shared address + stage_at(lane); p[i]: this lane's segment of the row's
+// first chunk; `in`: the segment is inside the row.  Segments past a row's end
+// are left as they are: their activations are zero, and the sums are of
+// integers.
+__device__ __forceinline__ void issue_chunk(uint32_t dst, const uint8_t* const (&p)[4], int c, bool in) {
     if (in) {
-        const int seg = lane & 7, r0 = lane >> 3;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(
-                             stage + (r0 + 4 * i) * 128 + ((seg ^ seg_perm(r0 + 4 * i)) << 4)),
-                         "l"(p + off[i])
+            asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"((dst ^ ((i & 1) << 5)) + 512 * i),
+                         "l"(p[i] + c * (kChunkK / 2))
                          : "memory");
     }
 }
 
-// Scales of a chunk's groups for the two rows g, g + 8 of a lane's quad: lane
-// q holds groups q and q + 4 of either row (fine groups), or group q & 1
-// (coarse ones).  s0, s8: index of the rows' first scale.
+// The scales of the rows g and g + 8 of a lane's quad.
+struct ScaleRows {
+    const char *p0, *p8;
+    __device__ __forceinline__ void open(const void* s, size_t row0, size_t row8, int G, int stype) {
+        const int sh = stype == kScaleF32 ? 2 : 1;
+        p0 = static_cast<const char*>(s) + ((row0 * G) << sh);
+        p8 = static_cast<const char*>(s) + ((row8 * G) << sh);
+    }
+};
+
+// Scales of chunk c's groups: lane q of a quad holds groups q and q + 4 (fine
+// groups), or group q & 1 (coarse ones) of row g in sc[0], sc[1] and of row g +
+// 8 in sc[2], sc[3]; 0 past the row's end.
 template <bool kCoarse>
-__device__ __forceinline__ void load_chunk_scales(float (&sc)[4], const void* s, size_t s0, size_t s8, int c, int gshift,
-                                                  int G, int stype, int q) {
-    if (kCoarse) {
-        const int i = min((c * kChunkK + (q & 1) * 128) >> gshift, G - 1);
-        sc[0] = load_scale(s, s0 + i, stype);
-        sc[2] = load_scale(s, s8 + i, stype);
+__device__ __forceinline__ void load_chunk_scales(float (&sc)[4], const ScaleRows& r, int c, int gshift, int G, int stype,
+                                                  int q) {
+    const int i = kCoarse ? min((c * kChunkK + (q & 1) * 128) >> gshift, G - 1) : ((c * kChunkK) >> gshift) + q;
+    const bool in0 = kCoarse || i < G, in1 = !kCoarse && gshift == 5 && i + 4 < G;
+    if (stype == kScaleF32) {
+        const float *a = reinterpret_cast<const float*>(r.p0) + i, *b = reinterpret_cast<const float*>(r.p8) + i;
+        sc[0] = in0 ? __ldg(a) : 0.f;
+        sc[2] = in0 ? __ldg(b) : 0.f;
+        sc[1] = in1 ? __ldg(a + 4) : 0.f;
+        sc[3] = in1 ? __ldg(b + 4) : 0.f;
     } else {
-        const int first = (c * kChunkK) >> gshift;
+        const unsigned short *a = reinterpret_cast<const unsigned short*>(r.p0) + i,
+                             *b = reinterpret_cast<const unsigned short*>(r.p8) + i;
+        // kept as raw bits until they are used (see scale_value)
+        sc[0] = __uint_as_float(in0 ? __ldg(a) : 0);
+        sc[2] = __uint_as_float(in0 ? __ldg(b) : 0);
+        sc[1] = __uint_as_float(in1 ? __ldg(a + 4) : 0);
+        sc[3] = __uint_as_float(in1 ? __ldg(b + 4) : 0);
+    }
+}
+
+// What load_chunk_scales left, as f32: converting there would wait for the load.
+__device__ __forceinline__ void scale_values(float (&sc)[4], int stype) {
+    if (stype == kScaleBf16) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int i = first + q + 4 * u;
-            const bool in = i < G && (u == 0 || gshift == 5);
-            sc[u] = in ? load_scale(s, s0 + i, stype) : 0.f;
-            sc[2 + u] = in ? load_scale(s, s8 + i, stype) : 0.f;
-        }
+        for (int i = 0; i < 4; ++i) sc[i] = __uint_as_float(__float_as_uint(sc[i]) << 16);
+    } else if (stype == kScaleF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = __half2float(__ushort_as_half((unsigned short)__float_as_uint(sc[i])));
     }
 }
 
@@ -183,7 +240,7 @@ template <int NT, bool kCoarse>
 __device__ __forceinline__ void chunk_mma(uint32_t stage, const uint32_t (&xb)[NT], const float (&sc)[4], int gshift,
                                           int lane, float (&t)[NT][2]) {
     const int g = lane >> 2, q = lane & 3, quad = lane & 28;
-    const uint32_t row = stage + g * 128 + (seg_perm(g) << 4);
+    const uint32_t row = stage + g * 128 + (seg_perm(g) << 4) + (kCoarse ? 0 : q * 4);
 #pragma unroll
     for (int n = 0; n < NT; ++n) t[n][0] = t[n][1] = 0.f;
     int d[NT][4];
@@ -211,7 +268,7 @@ __device__ __forceinline__ void chunk_mma(uint32_t stage, const uint32_t (&xb)[N
     } else {
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
-            const uint32_t at = (row ^ (b << 4)) + q * 4;
+            const uint32_t at = row ^ (b << 4);
             const uint32_t wa = lds32(at), wb = lds32(at + 1024);
             const uint32_t a[4] = {lo8(wa), lo8(wb), hi8(wa), hi8(wb)};
 #pragma unroll

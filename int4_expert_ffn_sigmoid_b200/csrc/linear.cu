@@ -45,54 +45,42 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
     const int tiles = p.tiles > (int)blockIdx.x ? (p.tiles - blockIdx.x - 1) / gridDim.x + 1 : 0;
     const int rows_cta = 16 << p.wr_log, last = a.N - 1, half = a.K / 2;
     int left = per * tiles;  // copies to issue
-
     int ir = blockIdx.x * rows_cta + team * 16, ic = j;  // row and chunk of the next copy
-    int off[4], islot = 0;
-    const uint8_t* ip;
-    auto tile_offsets = [&]() {  // rows past the last repeat it: their sums are not stored
-        const int r0 = min(ir, last);
+    uint32_t dst = ring + stage_at(lane);
+    const uint32_t dst_end = dst + kDepth * kStageBytes;
+    const uint8_t* ip[4];
+    auto open_tile = [&]() {  // rows past the last repeat it: their sums are not stored
 #pragma unroll
-        for (int i = 0; i < 4; ++i) off[i] = (min(ir + (lane >> 3) + 4 * i, last) - r0) * half;
-        ip = a.w + (size_t)r0 * half + (lane & 7) * 16;
+        for (int i = 0; i < 4; ++i) ip[i] = a.w + (size_t)min(ir + (lane >> 3) + 4 * i, last) * half + (lane & 7) * 16;
     };
     auto issue = [&]() {
         if (left > 0) {
             --left;
-            issue_chunk(ring + islot * kStageBytes, ip + ic * (kChunkK / 2), off, ic * kChunkK + (lane & 7) * 32 < a.K, lane);
-            islot = islot == kDepth - 1 ? 0 : islot + 1;
+            issue_chunk(dst, ip, ic, ic * kChunkK + (lane & 7) * 32 < a.K);
+            dst += kStageBytes;
+            if (dst == dst_end) dst -= kDepth * kStageBytes;
             ic += wk;
             if (ic >= p.chunks) {
                 ic = j;
                 ir += rows_cta * gridDim.x;
-                tile_offsets();
+                open_tile();
             }
         }
         cp_async_commit();
     };
     float nxt[4];
-    auto scales = [&](int row, int c) {
-        load_chunk_scales<kCoarse>(nxt, a.scales, (size_t)min(row + g, last) * a.G, (size_t)min(row + g + 8, last) * a.G, c,
-                                   a.gshift, a.G, a.stype, q);
-    };
+    ScaleRows sr;
+    auto open_scales = [&](int row) { sr.open(a.scales, min(row + g, last), min(row + g + 8, last), a.G, a.stype); };
+    auto scales = [&](int c) { load_chunk_scales<kCoarse>(nxt, sr, c, a.gshift, a.G, a.stype, q); };
     int row = ir;
-    tile_offsets();
+    open_tile();
     for (int i = 0; i < kDepth; ++i) issue();
-    if (per > 0 && tiles > 0) scales(row, j);
+    open_scales(row);
+    if (per > 0 && tiles > 0) scales(j);
     pdl_wait();
     pdl_release();
 
-    for (int t = 0, c = warp; t < p.nt;) {
-        if (c >= p.chunks) {
-            c -= p.chunks;
-            ++t;
-            continue;
-        }
-        const int k = c * kChunkK + 8 * lane;
-        const uint4 v = k < a.K ? __ldg(reinterpret_cast<const uint4*>(a.x + (p.t0 + t) * a.ldx + k)) : make_uint4(0, 0, 0, 0);
-        int8_t* r = xq + 2 * t * xs_bytes + c * kChunkK;
-        quantize_chunk<kCoarse>(v, r, r + xs_bytes, xs + c * 4 * NT + t, lane);
-        c += NW;
-    }
+    quantize_tokens<kCoarse>(a.x + p.t0 * a.ldx, a.ldx, a.K, p.chunks, p.nt, xq, xs_bytes, xs, 4 * NT, warp, NW, lane);
     __syncthreads();
 
     uint32_t xrow[NT];  // a column past the last token repeats it: its sums are not stored
@@ -110,8 +98,13 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
             float sc[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) sc[u] = nxt[u];
-            if (c + wk < p.chunks) scales(row, c + wk);
-            else if (i + 1 < tiles) scales(row + rows_cta * gridDim.x, j);
+            scale_values(sc, a.stype);
+            if (c + wk < p.chunks) {
+                scales(c + wk);
+            } else if (i + 1 < tiles) {
+                open_scales(row + rows_cta * gridDim.x);
+                scales(j);
+            }
             cp_async_wait<kDepth - 1>();
             __syncwarp();
             uint32_t xb[NT];
