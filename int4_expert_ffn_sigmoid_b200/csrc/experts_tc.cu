@@ -804,6 +804,17 @@ bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int esize, con
     return get_encode() && make_map(m, dt, esize, base, inner, rows, box_inner, box_rows, sw);
 }
 
+bool encode_tensor_map_rows(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+                            uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw) {
+    if (!get_encode()) return false;
+    cuuint64_t dims[2] = {inner, rows};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {box_inner, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return g_encode(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int tc_smem_bytes() { return tc::smem_bytes<4>(); }
 
 cudaError_t launch_tc_gemm(const Params& p, int gemm, int grid, cudaStream_t stream) {

@@ -53,6 +53,9 @@ struct FewArgs {
 int linear_launches(const LinearArgs& a);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
 
+// The tcgen05 GEMM of more tokens (linear_gemm.cu).
+cudaError_t launch_linear_gemm(const LinearArgs& a, cudaStream_t stream);
+
 int few_pass_tokens(const FewArgs& a);
 int few_pass_launches(const FewArgs& a);
 // Points a's workspace fields into ws (null: only measures); returns the bytes.

@@ -12,7 +12,7 @@ namespace moe {
 // fills it before waiting on the previous kernel: weights and scales are
 // constants, x and add are not.
 constexpr int kDepth = 3;
-constexpr int kPassTok = 8;
+constexpr int kStreamTok = 8;
 // Dynamic shared memory of one CTA at most, and of the activations alone.
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kXMax = 112 * 1024;
@@ -20,7 +20,6 @@ constexpr int kXMax = 112 * 1024;
 struct StreamPlan {
     int wk_log, wr_log;  // warps along the columns, teams: 1 << each
     int chunks, tiles;   // 256-column chunks of a row; CTA tiles of 16 rows a team
-    int t0, nt;          // the pass's first token and its tokens
 };
 
 template <int NW>
@@ -80,16 +79,16 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
     pdl_wait();
     pdl_release();
 
-    quantize_tokens<kCoarse>(a.x + p.t0 * a.ldx, a.ldx, a.K, p.chunks, p.nt, xq, xs_bytes, xs, 4 * NT, warp, NW, lane);
+    quantize_tokens<kCoarse>(a.x, a.ldx, a.K, p.chunks, a.T, xq, xs_bytes, xs, 4 * NT, warp, NW, lane);
     __syncthreads();
 
     uint32_t xrow[NT];  // a column past the last token repeats it: its sums are not stored
     const float* xsc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int t = min(4 * n + (g >> 1), p.nt - 1);
+        const int t = min(4 * n + (g >> 1), a.T - 1);
         xrow[n] = smem_addr(xq + (2 * t + (g & 1)) * xs_bytes);
-        xsc[n] = xs + min(4 * n + q, p.nt - 1);
+        xsc[n] = xs + min(4 * n + q, a.T - 1);
     }
     int slot = 0;
     for (int i = 0; i < tiles; ++i, row += rows_cta * gridDim.x) {
@@ -130,16 +129,15 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
             o[g + 8] = acc[n][1];
         }
         __syncthreads();
-        for (int o = tid; o < (p.nt * 16 << p.wr_log); o += 32 * NW) {
+        for (int o = tid; o < (a.T * 16 << p.wr_log); o += 32 * NW) {
             const int r = o & 15, tm = (o >> 4) & ((1 << p.wr_log) - 1), t = o >> (4 + p.wr_log);
             const int n = row - team * 16 + tm * 16 + r;
             if (n >= a.N) continue;
             float v = 0.f;
             for (int u = 0; u < wk; ++u) v += part[(((tm << p.wk_log) + u) * 4 * NT + t) * 16 + r];
-            const long long tt = p.t0 + t;
-            if (a.add) v += __bfloat162float(a.add[tt * a.lda + n]);
-            if (a.out_f32) static_cast<float*>(a.out)[tt * a.ldo + n] = v;
-            else static_cast<__nv_bfloat16*>(a.out)[tt * a.ldo + n] = __float2bfloat16_rn(v);
+            if (a.add) v += __bfloat162float(a.add[t * a.lda + n]);
+            if (a.out_f32) static_cast<float*>(a.out)[t * a.ldo + n] = v;
+            else static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + n] = __float2bfloat16_rn(v);
         }
     }
     cp_async_wait<0>();
@@ -160,9 +158,9 @@ int sms() {
 }
 
 template <int NW, int NT, bool kCoarse>
-cudaError_t launch_pass(const LinearArgs& a, StreamPlan p, cudaStream_t stream) {
+cudaError_t launch_stream(const LinearArgs& a, StreamPlan p, cudaStream_t stream) {
     const size_t smem = (size_t)NW * kDepth * kStageBytes + 2 * red_floats<NW>(4 * NT) * 4 + (size_t)p.chunks * 4 * NT * 4 +
-                        (size_t)p.nt * 2 * x_stride<kCoarse>(p.chunks);
+                        (size_t)a.T * 2 * x_stride<kCoarse>(p.chunks);
     auto* k = linear_stream_kernel<NW, NT, kCoarse>;
     static int set[64];
     int dev = 0;
@@ -178,35 +176,30 @@ cudaError_t launch_pass(const LinearArgs& a, StreamPlan p, cudaStream_t stream) 
 }
 
 template <int NW>
-cudaError_t launch_pass(const LinearArgs& a, const StreamPlan& p, cudaStream_t stream) {
+cudaError_t launch_stream(const LinearArgs& a, const StreamPlan& p, cudaStream_t stream) {
     const bool coarse = a.gshift >= 7;
-    if (p.nt <= 4) return coarse ? launch_pass<NW, 1, true>(a, p, stream) : launch_pass<NW, 1, false>(a, p, stream);
-    return coarse ? launch_pass<NW, 2, true>(a, p, stream) : launch_pass<NW, 2, false>(a, p, stream);
+    if (a.T <= 4) return coarse ? launch_stream<NW, 1, true>(a, p, stream) : launch_stream<NW, 1, false>(a, p, stream);
+    return coarse ? launch_stream<NW, 2, true>(a, p, stream) : launch_stream<NW, 2, false>(a, p, stream);
 }
 
-int pass_tokens(const LinearArgs& a) {
+int stream_tokens(const LinearArgs& a) {
     const int fit = kXMax / (2 * x_stride<true>((a.K + kChunkK - 1) / kChunkK));
-    return fit < kPassTok ? fit : kPassTok;
+    return fit < kStreamTok ? fit : kStreamTok;
 }
 
 }  // namespace
 
-int linear_launches(const LinearArgs& a) { return (a.T + pass_tokens(a) - 1) / pass_tokens(a); }
+int linear_launches(const LinearArgs&) { return 1; }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
+    if (a.T > stream_tokens(a)) return launch_linear_gemm(a, stream);
     StreamPlan p = {};
     p.chunks = (a.K + kChunkK - 1) / kChunkK;
-    const int pass = pass_tokens(a);
-    for (p.t0 = 0; p.t0 < a.T; p.t0 += pass) {
-        p.nt = a.T - p.t0 < pass ? a.T - p.t0 : pass;
-        const int nw_log = p.nt <= 2 ? 3 : 4;
-        for (p.wk_log = 0; p.wk_log < nw_log && (1 << p.wk_log) < p.chunks; ++p.wk_log) {}
-        if (p.wk_log > 3 && p.chunks < 32) p.wk_log = 3;
-        p.wr_log = nw_log - p.wk_log;
-        const cudaError_t e = nw_log == 3 ? launch_pass<8>(a, p, stream) : launch_pass<16>(a, p, stream);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    const int nw_log = a.T <= 2 ? 3 : 4;
+    for (p.wk_log = 0; p.wk_log < nw_log && (1 << p.wk_log) < p.chunks; ++p.wk_log) {}
+    if (p.wk_log > 3 && p.chunks < 32) p.wk_log = 3;
+    p.wr_log = nw_log - p.wk_log;
+    return nw_log == 3 ? launch_stream<8>(a, p, stream) : launch_stream<16>(a, p, stream);
 }
 
 }  // namespace moe

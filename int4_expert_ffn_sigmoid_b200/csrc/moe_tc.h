@@ -41,6 +41,10 @@ typedef CUresult (*PFN_encodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_
 bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, uint64_t inner,
                           uint64_t rows, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw);
 
+// The same with rows row_bytes apart (a multiple of 16).
+bool encode_tensor_map_rows(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+                            uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw);
+
 // Launch GEMM-1 (gemm = 1) or GEMM-2 (gemm = 2) of the large-batch path.
 cudaError_t launch_tc_gemm(const Params& p, int gemm, int grid, cudaStream_t stream);
 int tc_smem_bytes();
