@@ -63,14 +63,20 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, 
         "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
+// True on one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    const bool ok = *abort == 0 && bar_wait_or_abort(bar, parity, kWait, abort);
-    if (__all_sync(0xffffffffu, ok)) return true;
+    if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, bar_wait_or_abort(bar, parity, kWait, abort))) return true;
     *abort = 1;
     return false;
 }
@@ -142,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_slot;
     __shared__ int s_abort;
     volatile int* abort = &s_abort;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // warp-uniform to the compiler too: the MMA warp's descriptors then live in uniform registers
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     cg::cluster_group cluster = cg::this_cluster();
     const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const uint32_t ring = (smem_addr(dsm) + 1023u) & ~1023u;
@@ -209,31 +216,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bar_wait(full + i % G::kStages, (i / G::kStages) & 1, kWait);
         }
     } else if (warp == kConvWarps + 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16(kRows, kN);
-            bool ok = true;
-            for (int i = 0; i < n; ++i) {
-                const int s = i % G::kStages, sa = i % kAStages;
-                // a full A stage implies a landed ring stage for the converters; this thread reads x itself
-                ok = *abort == 0 && bar_wait_or_abort(full + s, (i / G::kStages) & 1, kWait, abort) &&
-                     bar_wait_or_abort(a_full + sa, (i / kAStages) & 1, kWait, abort);
-                if (!ok) break;
-                fence_after();
-                const uint32_t xs = ring + s * G::kStage + kWBytes, acol = tmem + kACol0 + sa * kACols;
+        // The whole warp runs the loop and one lane issues: under a divergent
+        // `lane == 0` every operand of an MMA is first moved to a uniform
+        // register (a stage of 16 MMAs took 1680 cycles, against LATER).
+        constexpr uint32_t idesc = idesc_bf16(kRows, kN);
+        const bool leader = elect_one();
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % G::kStages, sa = i % kAStages;
+            // a full A stage implies a landed ring stage for the converters; this warp's MMAs read x themselves
+            ok = warp_wait(full + s, (i / G::kStages) & 1, abort) && warp_wait(a_full + sa, (i / kAStages) & 1, abort);
+            if (!ok) break;
+            fence_after();
+            const uint64_t b0 = desc_sw128(ring + s * G::kStage + kWBytes);
+            const uint32_t acol = tmem + kACol0 + sa * kACols;
+            if (leader) {
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t b = desc_sw128(xs + kb * (G::kXBytes / 2) + kk * 32);
+                        const uint64_t b = b0 + ((kb * (G::kXBytes / 2) + kk * 32) >> 4);
                         mma_ts(tmem, acol + kb * 32 + kk * 8, b, idesc, (i | kb | kk) != 0);
                         mma_ts(tmem, acol + 64 + kb * 32 + kk * 8, b, idesc, 1);
                     }
                 commit(empty + s);
                 commit(a_empty + sa);
             }
-            if (!ok) *abort = 1;
-            commit(&done_bar);  // all MMAs issued are complete
+            __syncwarp();
         }
+        if (leader) commit(&done_bar);  // all MMAs issued are complete
     } else {
         // warp (group, half, quarter): rows 32 quarter .. + 31 (lane = row),
         // columns 64 half .. + 63 of the stages i = group mod 2
@@ -288,13 +299,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    pdl_wait();  // every thread that reads add or writes out below (the producer has waited: no-op there)
+    pdl_wait();  // for every thread that reads add or writes out below (the producer has waited: a no-op there)
     __syncwarp();
 
-    // Accumulators to registers: warp (quarter, cg): columns 8 c .. + 7, c = cg mod 4.
+    // Accumulators to registers: warp (quarter, cgrp): columns 8 c .. + 7, c = cgrp mod 4.
     constexpr int kChunks = kN / 8, kMine = (kChunks + 3) / 4;
-    float v[kMine][8];
     const int quarter = warp & 3, cgrp = warp >> 2;
+    float v[kMine][8];
+    // What the output rows already hold is loaded while the last MMAs run: at
+    // the store, one round trip to memory would follow another.
+    uint16_t plus[kMine][8];
+    auto inside = [&](int t, int row) { return t < a.T && row < a.N; };
+    // a cluster's rank owns the chunks c = rank mod size, thread by thread
+    const int own = (kChunks + size - 1 - rank) / size * 8 * kRows;
+    auto own_t = [&](int i) { return tok0 + 8 * (i / (8 * kRows) * size + rank) + i / kRows % 8; };
+    if (a.add && warp < kConvWarps) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                int t = tok0 + 8 * (cgrp + 4 * m) + u, row = row0 + quarter * 32 + lane;
+                bool in = cgrp + 4 * m < kChunks;
+                if (size > 1) {  // a rank's share is at most half as many elements
+                    const int i = threadIdx.x + (8 * m + u) * 32 * kConvWarps;
+                    t = own_t(i);
+                    row = row0 + i % kRows;
+                    in = i < own;
+                }
+                plus[m][u] = in && inside(t, row) ? __ldcg(reinterpret_cast<const unsigned short*>(a.add) + t * a.lda + row) : 0;
+            }
+    }
     if (warp < kConvWarps) {
         const bool ok = bar_wait(&done_bar, 0, kWait) && *abort == 0 && n > 0;
         const bool all = __all_sync(0xffffffffu, ok) != 0;
@@ -305,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c < kChunks) ld_tmem8(tmem + ((uint32_t)(quarter * 32) << 16) + 8 * c, v[m]);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (!all) v[m][u] = n > 0 ? __int_as_float(0x7fc00000) : 0.f;
+                if (!all) v[m][u] = __int_as_float(0x7fc00000);
         }
         fence_before();
     }
@@ -317,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
     }
-    auto store = [&](int t, int row, float y) {
-        if (t >= a.T || row >= a.N) return;
-        if (a.add) y += __bfloat162float(a.add[t * a.lda + row]);
+    auto store = [&](int t, int row, float y, uint16_t add) {
+        if (!inside(t, row)) return;
+        if (a.add) y += bf16lo(add);
         if (a.out_f32) static_cast<float*>(a.out)[t * a.ldo + row] = y;
         else static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + row] = __float2bfloat16_rn(y);
     };
@@ -329,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int m = 0; m < kMine; ++m)
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    if (cgrp + 4 * m < kChunks) store(tok0 + 8 * (cgrp + 4 * m) + u, row0 + quarter * 32 + lane, v[m][u]);
+                    if (cgrp + 4 * m < kChunks)
+                        store(tok0 + 8 * (cgrp + 4 * m) + u, row0 + quarter * 32 + lane, v[m][u], plus[m][u]);
         return;
     }
     // [chunk of this rank][source rank][token][row]
@@ -345,12 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < 8; ++u) to[u * kRows] = v[m][u];
         }
     cluster.sync();
-    for (int i = threadIdx.x; i < (kChunks + size - 1 - rank) / size * 8 * kRows; i += kThreads) {
-        const int r = i % kRows, u = i / kRows % 8, m = i / (8 * kRows);
-        float y = 0.f;
-        for (int q = 0; q < size; ++q) y += part[((size_t)(m * size + q) * 8 + u) * kRows + r];
-        store(tok0 + 8 * (m * size + rank) + u, row0 + r, y);
-    }
+    if (warp < kConvWarps)
+#pragma unroll
+        for (int e = 0; e < kMine * 8; ++e) {
+            const int i = threadIdx.x + e * 32 * kConvWarps;
+            if (i >= own) break;
+            float y = 0.f;
+            for (int q = 0; q < size; ++q) y += part[((size_t)(i / (8 * kRows) * size + q) * 8 + i / kRows % 8) * kRows + i % kRows];
+            store(own_t(i), row0 + i % kRows, y, plus[e / 8][e % 8]);
+        }
 }
 
 struct Capacity {
