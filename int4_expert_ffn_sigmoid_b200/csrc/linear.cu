@@ -4,7 +4,7 @@
 
 namespace moe {
 
-// Weight streaming for up to eight tokens a pass.  A CTA takes tiles of 16 *
+// Weight streaming for up to 16 tokens.  A CTA takes tiles of 16 *
 // wr rows; its warps are wr teams of wk, warp (team, j) multiplying the chunks
 // j, j + wk, ... of its team's 16 rows (chunk_mma) and the team's partial sums
 // meeting in shared memory.  Each warp runs its own ring of kDepth staged
@@ -12,10 +12,10 @@ namespace moe {
 // fills it before waiting on the previous kernel: weights and scales are
 // constants, x and add are not.
 constexpr int kDepth = 3;
-constexpr int kStreamTok = 8;
+constexpr int kStreamTok = 16;
 // Dynamic shared memory of one CTA at most, and of the activations alone.
 constexpr int kSmemMax = 227 * 1024;
-constexpr int kXMax = 112 * 1024;
+constexpr int kXMax = 96 * 1024;
 
 struct StreamPlan {
     int wk_log, wr_log;  // warps along the columns, teams: 1 << each
@@ -178,8 +178,11 @@ cudaError_t launch_stream(const LinearArgs& a, StreamPlan p, cudaStream_t stream
 template <int NW>
 cudaError_t launch_stream(const LinearArgs& a, const StreamPlan& p, cudaStream_t stream) {
     const bool coarse = a.gshift >= 7;
-    if (a.T <= 4) return coarse ? launch_stream<NW, 1, true>(a, p, stream) : launch_stream<NW, 1, false>(a, p, stream);
-    return coarse ? launch_stream<NW, 2, true>(a, p, stream) : launch_stream<NW, 2, false>(a, p, stream);
+    if constexpr (NW == 16) {
+        if (a.T > 8) return coarse ? launch_stream<NW, 4, true>(a, p, stream) : launch_stream<NW, 4, false>(a, p, stream);
+        if (a.T > 4) return coarse ? launch_stream<NW, 2, true>(a, p, stream) : launch_stream<NW, 2, false>(a, p, stream);
+    }
+    return coarse ? launch_stream<NW, 1, true>(a, p, stream) : launch_stream<NW, 1, false>(a, p, stream);
 }
 
 int stream_tokens(const LinearArgs& a) {

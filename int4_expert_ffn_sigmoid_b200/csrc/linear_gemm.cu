@@ -1,26 +1,27 @@
 // Dense projection with int4 weights and group scales for more tokens than
-// the weight-streaming kernel takes in a pass: a tcgen05 GEMM with the weights
-// as its M side.
+// the weight-streaming kernel takes: a tcgen05 GEMM with the weights as its M
+// side.
 //
 //   D[128 weight rows][kN tokens] += A[128][128 columns] x[kN][128 columns]^T
 //
 // per stage, accumulated in tensor memory over all columns (of this CTA's
-// share).  A is built in tensor memory from the packed codes: 16 converter
+// share).  A is built in tensor memory from the packed codes: the converter
 // warps turn a row's codes into bf16 and multiply them by the row's group
-// scale.  A bf16 product alone would round every weight by up to 2^-9, as much
-// as the output's own rounding; the rest goes into a second bf16 matrix,
-//   hi = bf16(c s),  lo = bf16(c s - hi)        (exact to 2^-16 of the weight)
-// and each k step takes two MMAs, hi x + lo x.  The second MMA is free until
-// the tensor pipe bounds the kernel (a few hundred tokens), and x enters as it
-// is, by TMA.  A scale of 24 or 11 bits is itself split in two bf16 parts.
+// scale, rounding each weight once (2^-8 of it at most; the codes 0, 1, 2, 4
+// and 8 times a bf16 scale are exact).  x enters as it is, by TMA.  A second
+// MMA per step with what the rounding left (exact to 2^-16) was built first
+// and taken out: an MMA with A in tensor memory takes 69 cycles at 64 tokens
+// and 84 at 128, so it held the kernel to the MMAs' pace (23.5 against 19.1 us
+// for 64 tokens x 6144 x 6144, 40.3 against 30.0 for 512 x 4096 x 6144) while
+// the bf16 output's own rounding (1.66e-3) is over twice what it removed.
 //
 // Few row tiles: a cluster of up to eight CTAs shares a tile's columns, sums
 // its parts in shared memory (rank c % size takes tokens 8 c .. 8 c + 7) and
 // stores them; in the same order every time.
 //
-// Roles (576 threads, one CTA per SM): warps 0-15 convert (groups of eight
-// take alternate stages) and then read the accumulators out; warp 16 issues
-// the TMA loads, warp 17 the MMAs.  Every wait is bounded; a CTA whose wait
+// Roles (864 threads, one CTA per SM): warps 0-23 convert (three groups of
+// eight take the stages in turn) and then read the accumulators out; warps 24
+// and 25 issue the TMA loads of the codes and of x, warp 26 the MMAs.  Every wait is bounded; a CTA whose wait
 // gave up (never, in a correct run) stores NaN.
 #include <cooperative_groups.h>
 #include <cuda.h>
@@ -32,21 +33,27 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 128, kStageK = 128;
-constexpr int kConvWarps = 16, kThreads = 32 * (kConvWarps + 2);
-constexpr int kAStages = 3, kACols = 128, kACol0 = 128;  // tensor memory: D in columns 0-127, then the A stages
+constexpr int kGroups = 3, kConvWarps = 8 * kGroups, kThreads = 32 * (kConvWarps + 3);
+constexpr int kWarpW = kConvWarps, kWarpX = kConvWarps + 1, kWarpMma = kConvWarps + 2;
+constexpr int kColGroups = kConvWarps / 4;  // warps of a lane quarter, for reading the accumulators
+constexpr int kACols = 64, kACol0 = 256;  // tensor memory: D in columns 0-255, then the A stages
 constexpr int kTmemCols = 512;
 constexpr int kWBytes = kRows * kStageK / 2;
 constexpr long long kWait = kBulkWaitCycles;
 
 template <int kN>
 struct Geo {
+    // Stages of x and of A go together: the one commit after a stage's MMAs
+    // frees both.  The codes have a deeper ring of their own.
     static constexpr int kXBytes = kN * kStageK * 2;
-    static constexpr int kStage = kWBytes + kXBytes;
-    static constexpr int kStages = kN == 128 ? 4 : kN == 64 ? 6 : 8;
-    static constexpr int kRing = kStages * kStage;
-    static constexpr int kSmem = kRing + 1024 + 512;
-    // the cluster's partial sums reuse the ring: chunks of 8 tokens, rounded up per rank
-    static_assert((kN / 8 + 7) * 8 * kRows * 4 <= kRing, "partial sums fit the ring");
+    static constexpr int kStages = kN == 256 ? 3 : 4;
+    static constexpr int kWStages = kN == 256 ? 4 : 8;
+    static constexpr int kRing = kStages * kXBytes + kWStages * kWBytes;
+    // over half of an SM's: two CTAs there would wait on each other's tensor memory
+    static constexpr int kSmem = kRing + 1024 > 116 * 1024 ? kRing + 1024 : 116 * 1024;
+    static_assert(kACol0 + kStages * kACols <= kTmemCols, "tensor memory");
+    // the cluster's partial sums reuse the rings: chunks of 8 tokens, rounded up per rank
+    static_assert((kN / 8 + 7) * 8 * kRows * 4 <= kRing, "partial sums fit the rings");
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
@@ -105,30 +112,33 @@ __device__ __forceinline__ void ld_tmem8(uint32_t at, float (&v)[8]) {
 struct ScaleParts {
     __nv_bfloat162 hi, lo;
 };
+template <bool kLow>
 __device__ __forceinline__ ScaleParts split_scale(uint32_t raw, int stype) {
-    const float s = stype == kScaleF32   ? __uint_as_float(raw)
-                    : stype == kScaleBf16 ? __uint_as_float(raw << 16)
-                                          : __half2float(__ushort_as_half((unsigned short)raw));
+    if (!kLow) {  // bf16 scales
+        const uint32_t two = __byte_perm(raw, 0, 0x1010);
+        const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&two);
+        return {s, s};
+    }
+    const float s = stype == kScaleF32 ? __uint_as_float(raw) : __half2float(__ushort_as_half((unsigned short)raw));
     ScaleParts p;
     p.hi = __float2bfloat162_rn(s);
     p.lo = __float2bfloat162_rn(s - __low2float(p.hi));
     return p;
 }
 
-// Eight codes times a scale: four words of bf16 pairs in column order, and
-// what they lack.  kLow: the scale has a low part.
+// Eight codes times a scale: four words of bf16 pairs in column order.
+// kLow: the scale has a low part.
 template <bool kLow>
-__device__ __forceinline__ void dequant8(uint32_t w, const ScaleParts& s, uint32_t* hi, uint32_t* lo) {
-    uint32_t c[4];
-    int4x8_to_16<true>(w, c);
+__device__ __forceinline__ void dequant8(uint32_t w, const ScaleParts& s, uint32_t* o) {
+    const uint32_t w4 = w >> 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&c[j]);
-        const __nv_bfloat162 h = __hmul2(v, s.hi);
-        __nv_bfloat162 l = __hfma2(v, s.hi, __hneg2(h));  // exact: a 4-bit by an 8-bit value has 12 bits
-        if (kLow) l = __hfma2(v, s.lo, l);
-        hi[j] = *reinterpret_cast<const uint32_t*>(&h);
-        lo[j] = *reinterpret_cast<const uint32_t*>(&l);
+        // int4x8_to_16 with the sign flip folded into the mask's operation: 128 + 8 + c, minus 136
+        const uint32_t t = (__byte_perm(w, w4, j | ((4 + j) << 8)) & 0x000f000fu) ^ 0x43084308u;
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&t),
+                                         __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)));
+        const __nv_bfloat162 h = kLow ? __hfma2(v, s.hi, __hmul2(v, s.lo)) : __hmul2(v, s.hi);
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
 }
 
@@ -144,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     namespace cg = cooperative_groups;
     using G = Geo<kN>;
     extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ uint64_t full[G::kStages], empty[G::kStages], a_full[kAStages], a_empty[kAStages], done_bar;
+    __shared__ uint64_t w_full[G::kWStages], w_empty[G::kWStages], x_full[G::kStages], a_full[G::kStages], empty[G::kStages], done_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int s_abort;
     volatile int* abort = &s_abort;
@@ -159,19 +169,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = st1 - st0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < G::kStages; ++i) {
-            bar_init(full + i, 1);
-            bar_init(empty + i, 1 + 8);  // the MMAs' commit, a group's converter warps
+        for (int i = 0; i < G::kWStages; ++i) {
+            bar_init(w_full + i, 1);
+            bar_init(w_empty + i, 8);  // a group's converter warps
         }
-        for (int i = 0; i < kAStages; ++i) {
+        for (int i = 0; i < G::kStages; ++i) {
+            bar_init(x_full + i, 1);
             bar_init(a_full + i, 8);
-            bar_init(a_empty + i, 1);
+            bar_init(empty + i, 1);  // the MMAs' commit
         }
         bar_init(&done_bar, 1);
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kConvWarps + 1) {
+    if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
                      "n"(kTmemCols)
                      : "memory");
@@ -182,54 +193,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = tmem_slot;
 
-    if (warp == kConvWarps) {
-        if (lane == 0) {
-            auto load_w = [&](int i) {
-                const int s = i % G::kStages;
-                bar_expect_tx(full + s, G::kStage);
-                tma_tile(ring_p + s * G::kStage, &map_w, full + s, (st0 + i) * (kStageK / 2), row0);
-            };
-            auto load_x = [&](int i) {
-                const int s = i % G::kStages;
-                uint8_t* x = ring_p + s * G::kStage + kWBytes;
-                tma_tile(x, &map_x, full + s, (st0 + i) * kStageK, tok0);
-                tma_tile(x + G::kXBytes / 2, &map_x, full + s, (st0 + i) * kStageK + 64, tok0);
-            };
-            // the weights do not depend on the kernel before this one, x does
-            const int early = n < G::kStages ? n : G::kStages;
-            for (int i = 0; i < early; ++i) load_w(i);
-            pdl_wait();
-            pdl_release();
-            int issued = early;
-            for (int i = 0; i < early; ++i) load_x(i);
-            for (int i = early; i < n; ++i) {
-                if (*abort || !bar_wait_or_abort(empty + i % G::kStages, (i / G::kStages - 1) & 1, kWait, abort)) {
+    uint8_t* const xring = ring_p;
+    uint8_t* const wring = ring_p + G::kStages * G::kXBytes;
+    if (warp == kWarpW) {
+        if (lane == 0) {  // weights do not depend on the kernel before this one
+            int i = 0;
+            for (; i < n; ++i) {
+                const int s = i % G::kWStages;
+                if (i >= G::kWStages && !bar_wait_or_abort(w_empty + s, (i / G::kWStages - 1) & 1, kWait, abort)) {
                     *abort = 1;
                     break;
                 }
-                load_w(i);
-                load_x(i);
-                ++issued;
+                bar_expect_tx(w_full + s, kWBytes);
+                tma_tile(wring + s * kWBytes, &map_w, w_full + s, (st0 + i) * (kStageK / 2), row0);
             }
             // every copy lands before the CTA's shared memory is reused or goes away
-            for (int i = issued > G::kStages ? issued - G::kStages : 0; i < issued; ++i)
-                bar_wait(full + i % G::kStages, (i / G::kStages) & 1, kWait);
+            for (int j = i > G::kWStages ? i - G::kWStages : 0; j < i; ++j)
+                bar_wait(w_full + j % G::kWStages, (j / G::kWStages) & 1, kWait);
         }
-    } else if (warp == kConvWarps + 1) {
+    } else if (warp == kWarpX) {
+        if (lane == 0) {
+            pdl_wait();
+            pdl_release();
+            int i = 0;
+            for (; i < n; ++i) {
+                const int s = i % G::kStages;
+                if (i >= G::kStages && !bar_wait_or_abort(empty + s, (i / G::kStages - 1) & 1, kWait, abort)) {
+                    *abort = 1;
+                    break;
+                }
+                bar_expect_tx(x_full + s, G::kXBytes);
+                uint8_t* x = xring + s * G::kXBytes;
+                tma_tile(x, &map_x, x_full + s, (st0 + i) * kStageK, tok0);
+                tma_tile(x + G::kXBytes / 2, &map_x, x_full + s, (st0 + i) * kStageK + 64, tok0);
+            }
+            for (int j = i > G::kStages ? i - G::kStages : 0; j < i; ++j)
+                bar_wait(x_full + j % G::kStages, (j / G::kStages) & 1, kWait);
+        }
+    } else if (warp == kWarpMma) {
         // The whole warp runs the loop and one lane issues: under a divergent
         // `lane == 0` every operand of an MMA is first moved to a uniform
-        // register (a stage of 16 MMAs took 1680 cycles, against LATER).
+        // register (16 MMAs took 1130 cycles to issue, against 560).
         constexpr uint32_t idesc = idesc_bf16(kRows, kN);
         const bool leader = elect_one();
         bool ok = true;
         for (int i = 0; i < n; ++i) {
-            const int s = i % G::kStages, sa = i % kAStages;
-            // a full A stage implies a landed ring stage for the converters; this warp's MMAs read x themselves
-            ok = warp_wait(full + s, (i / G::kStages) & 1, abort) && warp_wait(a_full + sa, (i / kAStages) & 1, abort);
+            const int s = i % G::kStages;
+            const uint32_t ph = (i / G::kStages) & 1;
+            const bool ready = bar_try(x_full + s, ph) & bar_try(a_full + s, ph);
+            ok = __all_sync(0xffffffffu, ready) || (warp_wait(x_full + s, ph, abort) && warp_wait(a_full + s, ph, abort));
             if (!ok) break;
             fence_after();
-            const uint64_t b0 = desc_sw128(ring + s * G::kStage + kWBytes);
-            const uint32_t acol = tmem + kACol0 + sa * kACols;
+            const uint64_t b0 = desc_sw128(ring + s * G::kXBytes);
+            const uint32_t acol = tmem + kACol0 + s * kACols;
             if (leader) {
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
@@ -237,17 +253,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint64_t b = b0 + ((kb * (G::kXBytes / 2) + kk * 32) >> 4);
                         mma_ts(tmem, acol + kb * 32 + kk * 8, b, idesc, (i | kb | kk) != 0);
-                        mma_ts(tmem, acol + 64 + kb * 32 + kk * 8, b, idesc, 1);
                     }
                 commit(empty + s);
-                commit(a_empty + sa);
             }
             __syncwarp();
         }
         if (leader) commit(&done_bar);  // all MMAs issued are complete
     } else {
         // warp (group, half, quarter): rows 32 quarter .. + 31 (lane = row),
-        // columns 64 half .. + 63 of the stages i = group mod 2
+        // columns 64 half .. + 63 of the stages i = group mod kGroups
         const int quarter = warp & 3, half = (warp >> 2) & 1, group = warp >> 3;
         const int row = min(row0 + quarter * 32 + lane, a.N - 1);
         const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + kACol0 + half * 32;
@@ -267,67 +281,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         raw[0] = raw[1] = 0;
         if (group < n) load_scales(group);
-        for (int i = group; i < n; i += 2) {
-            const int s = i % G::kStages, sa = i % kAStages;
+        for (int i = group; i < n; i += kGroups) {
+            const int s = i % G::kStages, sw = i % G::kWStages;
             ScaleParts sp[2];
-            sp[0] = split_scale(raw[0], a.stype);
-            sp[1] = two ? split_scale(raw[1], a.stype) : sp[0];
-            if (i + 2 < n) load_scales(i + 2);
-            if (!warp_wait(full + s, (i / G::kStages) & 1, abort)) break;
+            sp[0] = split_scale<kLow>(raw[0], a.stype);
+            sp[1] = two ? split_scale<kLow>(raw[1], a.stype) : sp[0];
+            if (i + kGroups < n) load_scales(i + kGroups);
+            const uint32_t full_ph = (i / G::kWStages) & 1, free_ph = ((i / G::kStages) & 1) ^ 1u;
+            // usually both are ready: one round trip to the barriers, not two
+            const bool ready = bar_try(w_full + sw, full_ph) & bar_try(empty + s, free_ph);
+            if (!__all_sync(0xffffffffu, ready) &&
+                !(warp_wait(w_full + sw, full_ph, abort) && warp_wait(empty + s, free_ph, abort)))
+                break;
             uint4 w[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u)  // 16-byte chunk 2 half + u of the row's 64 bytes (64-byte swizzle)
-                w[u] = lds128(ring + s * G::kStage + r * 64 + (((2 * half + u) ^ ((r >> 1) & 3)) << 4));
-            if (!warp_wait(a_empty + sa, ((i / kAStages) & 1) ^ 1u, abort)) break;
+                w[u] = lds128(smem_addr(wring) + sw * kWBytes + r * 64 + (((2 * half + u) ^ ((r >> 1) & 3)) << 4));
             fence_after();
-            uint32_t hi[32], lo[32];
+            uint32_t o[32];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                dequant8<kLow>(w[u].x, sp[u], hi + 16 * u, lo + 16 * u);
-                dequant8<kLow>(w[u].y, sp[u], hi + 16 * u + 4, lo + 16 * u + 4);
-                dequant8<kLow>(w[u].z, sp[u], hi + 16 * u + 8, lo + 16 * u + 8);
-                dequant8<kLow>(w[u].w, sp[u], hi + 16 * u + 12, lo + 16 * u + 12);
+                dequant8<kLow>(w[u].x, sp[u], o + 16 * u);
+                dequant8<kLow>(w[u].y, sp[u], o + 16 * u + 4);
+                dequant8<kLow>(w[u].z, sp[u], o + 16 * u + 8);
+                dequant8<kLow>(w[u].w, sp[u], o + 16 * u + 12);
             }
-            st_tmem32(at + sa * kACols, hi);
-            st_tmem32(at + sa * kACols + 64, lo);
+            st_tmem32(at + s * kACols, o);
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before();
             __syncwarp();
             if (lane == 0) {
-                bar_arrive(a_full + sa);
-                bar_arrive(empty + s);
+                bar_arrive(a_full + s);
+                bar_arrive(w_empty + sw);
             }
         }
     }
     pdl_wait();  // for every thread that reads add or writes out below (the producer has waited: a no-op there)
     __syncwarp();
 
-    // Accumulators to registers: warp (quarter, cgrp): columns 8 c .. + 7, c = cgrp mod 4.
-    constexpr int kChunks = kN / 8, kMine = (kChunks + 3) / 4;
+    // Accumulators to registers: warp (quarter, cgrp): columns 8 c .. + 7, c = cgrp mod kColGroups.
+    constexpr int kChunks = kN / 8, kMine = (kChunks + kColGroups - 1) / kColGroups;
     const int quarter = warp & 3, cgrp = warp >> 2;
     float v[kMine][8];
-    // What the output rows already hold is loaded while the last MMAs run: at
-    // the store, one round trip to memory would follow another.
-    uint16_t plus[kMine][8];
     auto inside = [&](int t, int row) { return t < a.T && row < a.N; };
-    // a cluster's rank owns the chunks c = rank mod size, thread by thread
+    // Element u of group m of this thread: of its accumulators or, in a
+    // cluster, of the rank's chunks c = rank mod size, a CTA's worth at a time
+    // (at most half as many groups).
     const int own = (kChunks + size - 1 - rank) / size * 8 * kRows;
-    auto own_t = [&](int i) { return tok0 + 8 * (i / (8 * kRows) * size + rank) + i / kRows % 8; };
-    if (a.add && warp < kConvWarps) {
+    struct Place {
+        int t, row;
+        bool in;
+    };
+    auto place = [&](int m, int u) {
+        Place p;
+        if (size == 1) {
+            p.t = tok0 + 8 * (cgrp + kColGroups * m) + u;
+            p.row = row0 + quarter * 32 + lane;
+            p.in = cgrp + kColGroups * m < kChunks && inside(p.t, p.row);
+        } else {
+            const int i = threadIdx.x + (8 * m + u) * 32 * kConvWarps;
+            p.t = tok0 + 8 * (i / (8 * kRows) * size + rank) + i / kRows % 8;
+            p.row = row0 + i % kRows;
+            p.in = i < own && inside(p.t, p.row);
+        }
+        return p;
+    };
+    auto load_add = [&](int m, uint16_t (&o)[8]) {
 #pragma unroll
-        for (int m = 0; m < kMine; ++m)
+        for (int u = 0; u < 8; ++u) {
+            const Place p = place(m, u);
+            o[u] = a.add && p.in ? __ldcg(reinterpret_cast<const unsigned short*>(a.add) + p.t * a.lda + p.row) : 0;
+        }
+    };
+    // Up to 128 tokens, add is loaded while the last MMAs run; eight loads at a time otherwise (registers).
+    constexpr int kEarly = kN <= 128 ? kMine : 0;
+    uint16_t plus[kMine][8];
+    if (warp < kConvWarps) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                int t = tok0 + 8 * (cgrp + 4 * m) + u, row = row0 + quarter * 32 + lane;
-                bool in = cgrp + 4 * m < kChunks;
-                if (size > 1) {  // a rank's share is at most half as many elements
-                    const int i = threadIdx.x + (8 * m + u) * 32 * kConvWarps;
-                    t = own_t(i);
-                    row = row0 + i % kRows;
-                    in = i < own;
-                }
-                plus[m][u] = in && inside(t, row) ? __ldcg(reinterpret_cast<const unsigned short*>(a.add) + t * a.lda + row) : 0;
-            }
+        for (int m = 0; m < kEarly; ++m) load_add(m, plus[m]);
     }
     if (warp < kConvWarps) {
         const bool ok = bar_wait(&done_bar, 0, kWait) && *abort == 0 && n > 0;
@@ -335,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-            const int c = cgrp + 4 * m;
+            const int c = cgrp + kColGroups * m;
             if (c < kChunks) ld_tmem8(tmem + ((uint32_t)(quarter * 32) << 16) + 8 * c, v[m]);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
@@ -345,26 +376,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     // Tensor memory is freed before any wait on another CTA.
-    if (warp == kConvWarps + 1) {
+    if (warp == kWarpMma) {
         bar_wait(&done_bar, 0, kWait);
         __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
     }
-    auto store = [&](int t, int row, float y, uint16_t add) {
-        if (!inside(t, row)) return;
-        if (a.add) y += bf16lo(add);
-        if (a.out_f32) static_cast<float*>(a.out)[t * a.ldo + row] = y;
-        else static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + row] = __float2bfloat16_rn(y);
+    auto store = [&](int m, const float (&y)[8]) {
+        if (m >= kEarly) load_add(m, plus[m]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const Place p = place(m, u);
+            const float o = a.add ? y[u] + bf16lo(plus[m][u]) : y[u];
+            if (!p.in) continue;
+            if (a.out_f32) static_cast<float*>(a.out)[p.t * a.ldo + p.row] = o;
+            else static_cast<__nv_bfloat16*>(a.out)[p.t * a.ldo + p.row] = __float2bfloat16_rn(o);
+        }
     };
     if (size == 1) {
         if (warp < kConvWarps)
 #pragma unroll
-            for (int m = 0; m < kMine; ++m)
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (cgrp + 4 * m < kChunks)
-                        store(tok0 + 8 * (cgrp + 4 * m) + u, row0 + quarter * 32 + lane, v[m][u], plus[m][u]);
+            for (int m = 0; m < kMine; ++m) store(m, v[m]);
         return;
     }
     // [chunk of this rank][source rank][token][row]
@@ -373,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kConvWarps)
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-            const int c = cgrp + 4 * m;
+            const int c = cgrp + kColGroups * m;
             if (c >= kChunks) continue;
             float* to = cluster.map_shared_rank(part, c % size) + ((size_t)(c / size) * size + rank) * 8 * kRows + quarter * 32 + lane;
 #pragma unroll
@@ -382,12 +414,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster.sync();
     if (warp < kConvWarps)
 #pragma unroll
-        for (int e = 0; e < kMine * 8; ++e) {
-            const int i = threadIdx.x + e * 32 * kConvWarps;
-            if (i >= own) break;
-            float y = 0.f;
-            for (int q = 0; q < size; ++q) y += part[((size_t)(i / (8 * kRows) * size + q) * 8 + i / kRows % 8) * kRows + i % kRows];
-            store(own_t(i), row0 + i % kRows, y, plus[e / 8][e % 8]);
+        for (int m = 0; m < kMine; ++m) {
+            if (8 * m * 32 * kConvWarps >= own) break;
+            float y[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int i = threadIdx.x + (8 * m + u) * 32 * kConvWarps;
+                y[u] = 0.f;
+                if (i < own)
+                    for (int q = 0; q < size; ++q)
+                        y[u] += part[((size_t)(i / (8 * kRows) * size + q) * 8 + i / kRows % 8) * kRows + i % kRows];
+            }
+            store(m, y);
         }
 }
 
@@ -464,7 +502,8 @@ cudaError_t launch_linear_gemm(const LinearArgs& a, cudaStream_t stream) {
     if (a.T <= 16) return low ? launch<16, true>(a, stream) : launch<16, false>(a, stream);
     if (a.T <= 32) return low ? launch<32, true>(a, stream) : launch<32, false>(a, stream);
     if (a.T <= 64) return low ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
-    return low ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+    if (a.T <= 128) return low ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+    return low ? launch<256, true>(a, stream) : launch<256, false>(a, stream);
 }
 
 }  // namespace moe
