@@ -22,12 +22,10 @@
 
 namespace moe {
 
-constexpr int kFewTok = 8;
 constexpr int kFewWarps = 16;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewDepth = 3;
 constexpr int kFewTileRows = 32;  // h elements of a gate/up tile
-constexpr int kFewMaxU = kFewTok * kMaxK;
 constexpr int kFewSmemMax = 227 * 1024;
 constexpr int kFewXMax = 98 * 1024;
 // CTAs that share the router: a cluster of kFewCluster computes all logits,
@@ -41,89 +39,40 @@ constexpr int kFewRouterMax = 128 * 1024;
 bool few_split_router(int E, int H) { return (size_t)E * H * 4 > (size_t)kFewCluster * kFewRouterMax; }
 int few_logit_slices(int H) { return (H / 128 + 2) / 3; }
 
-// What the picks of a pass come to, in shared memory.
-struct FewPicks {
-    unsigned mask[kMaxE / 32];       // touched experts
-    int U;                           // their number
-    int expert[kFewMaxU];            // ascending
-    int8_t slot[kFewMaxU][kFewTok];  // t * K + k of token t's pick of the expert, or -1
-    float weight[kFewMaxU][kFewTok];
-    unsigned tokens[kFewMaxU];       // bit t: token t picked it
-};
-
-// Builds P from the picks (idx, wts: T * K <= 64 values, one per thread of the
-// first two warps; -1: dropped).  All threads of the CTA.
-__device__ __forceinline__ void few_gather(FewPicks& P, int T, int K, int my_e, float my_w) {
-    const int tid = threadIdx.x;
-    if (tid < kMaxE / 32) P.mask[tid] = 0;
-    __syncthreads();
-    const bool mine = tid < T * K && my_e >= 0;
-    if (mine) atomicOr(&P.mask[my_e >> 5], 1u << (my_e & 31));
-    for (int i = tid; i < kFewMaxU * kFewTok; i += kFewThreads) P.slot[i / kFewTok][i % kFewTok] = -1;
-    if (tid < kFewMaxU) P.tokens[tid] = 0;
-    __syncthreads();
-    auto rank = [&](int e) {
-        int r = 0;
-        for (int i = 0; i < (e >> 5); ++i) r += __popc(P.mask[i]);
-        return r + __popc(P.mask[e >> 5] & ((1u << (e & 31)) - 1));
-    };
-    if (mine) {
-        const int u = rank(my_e), t = tid / K;
-        P.expert[u] = my_e;
-        P.slot[u][t] = (int8_t)tid;
-        P.weight[u][t] = my_w;
-        atomicOr(&P.tokens[u], 1u << t);
-    }
-    if (tid == 0) {
-        int n = 0;
-        for (int i = 0; i < kMaxE / 32; ++i) n += __popc(P.mask[i]);
-        P.U = n;
-    }
-    __syncthreads();
-}
-
 __device__ __forceinline__ uint32_t ordered(float f) {
     const uint32_t b = __float_as_uint(f);
     return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
-// Top-K of one token (one warp) from its logits in shared memory: the K
-// largest sigmoid(L) + bias, ties to the lower expert, NaN as -infinity.
-// Lane k < K returns pick k and its weight.
-__device__ __forceinline__ void few_select(const FewArgs& a, const float* lg, int lane, int& out_e, float& out_w) {
+// Top-K of one token (one warp) from its scores in shared memory: the K
+// largest score + bias (NaN as -infinity), ties to the lower expert.  Lane k <
+// K returns pick k and its weight.
+__device__ __forceinline__ void few_select(const FewArgs& a, const float* scores, const float* bias, int lane, int& out_e,
+                                           float& out_w) {
     uint32_t key[kMaxE / 32];
-    float sc[kMaxE / 32];
 #pragma unroll
     for (int j = 0; j < kMaxE / 32; ++j) {
         const int e = lane + 32 * j;
-        key[j] = 0;  // below every key: -infinity is 0x007fffff
-        sc[j] = 0.f;
-        if (e < a.E) {
-            sc[j] = 1.0f / (1.0f + expf(-lg[e]));
-            const float k = sc[j] + __ldg(a.rb + e);
-            key[j] = ordered(isnan(k) ? -INFINITY : k + 0.0f);  // + 0: -0 compares as 0
-        }
+        const float k = e < a.E ? scores[e] + bias[e] : 0.f;
+        key[j] = e < a.E ? ordered(isnan(k) ? -INFINITY : k + 0.0f) : 0;  // + 0: -0 compares as 0; 0: below every key
     }
     int my_e = -1;
     float my_s = 0.f, ssum = 0.f;
+#pragma unroll 1
     for (int k = 0; k < a.K; ++k) {
         uint32_t best = 0;
 #pragma unroll
         for (int j = 0; j < kMaxE / 32; ++j) best = max(best, key[j]);
         best = __reduce_max_sync(0xffffffffu, best);
-        int e = 0x7fffffff;
-        float s = 0.f;
+        unsigned e = 0x7fffffff;
 #pragma unroll
         for (int j = kMaxE / 32 - 1; j >= 0; --j)
-            if (key[j] == best && lane + 32 * j < a.E) {
-                e = lane + 32 * j;
-                s = sc[j];
-            }
-        const int be = (int)__reduce_min_sync(0xffffffffu, (unsigned)e);
-        s = __shfl_sync(0xffffffffu, s, be & 31);
+            if (key[j] == best) e = lane + 32 * j;
+        const int be = (int)__reduce_min_sync(0xffffffffu, e);
 #pragma unroll
         for (int j = 0; j < kMaxE / 32; ++j)
             if (lane + 32 * j == be) key[j] = 0;
+        const float s = scores[be];
         if (lane == k) {
             my_e = be;
             my_s = s;
@@ -138,9 +87,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     namespace cg = cooperative_groups;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ FewPicks P;
-    __shared__ float s_logit[kFewTok][kMaxE];
-    __shared__ int s_e[kFewMaxU];
-    __shared__ float s_w[kFewMaxU];
+    __shared__ float s_logit[kFewTok][kMaxE];  // logits, then scores
+    __shared__ float s_bias[kMaxE];
+    __shared__ unsigned s_mask[kMaxE / 32];  // touched experts
+    __shared__ float s_weight[kFewMaxU][kFewTok];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
@@ -217,81 +167,133 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     open_tile();
     for (int i = 0; i < kFewDepth; ++i) issue();
 
+    // Before the wait: the router's constants, and the tables' initial state.
+    const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int epc = (a.E + size - 1) / size, e_lo = rank * epc, e_hi = min(a.E, e_lo + epc);
+    if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started
+    if (tid < a.E) s_bias[tid] = __ldg(a.rb + tid);
+    if (tid < kMaxE / 32) s_mask[tid] = 0;
+    if (tid < kFewMaxU) P.tokens[tid] = 0;
+    P.slot[tid / kFewTok][tid % kFewTok] = -1;
+    static_assert(kFewThreads == kFewMaxU * kFewTok, "one slot a thread");
+    // The dot product of this warp's experts e_lo + warp, + 16, ...: eight
+    // 128-column blocks of weights at a time, the next ones on their way.
+    float4 wn[8];
+    auto load_w = [&](int e, int b) {
+        const float4* w = reinterpret_cast<const float4*>(a.rw + (size_t)e * H) + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wn[i] = b + i < H / 128 ? __ldg(w + (b + i) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    int e = a.lslices > 0 ? e_hi : e_lo + warp;
+    if (e < e_hi) load_w(e, 0);
     pdl_wait();
     pdl_release();
 
+    // x in shared memory where it fits the room of the partial sums
+    const __nv_bfloat16* x = a.x;
+    if ((size_t)T * H * 2 <= 2 * kRed * 4) {
+        __nv_bfloat16* xr = reinterpret_cast<__nv_bfloat16*>(red);
+        for (int i = tid; i < T * H / 8; i += kFewThreads)
+            reinterpret_cast<uint4*>(xr)[i] = __ldg(reinterpret_cast<const uint4*>(a.x) + i);
+        x = xr;
+        __syncthreads();
+    }
+    if (size > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+
     // Router logits of this CTA's experts, to every CTA of the cluster.
-    {
-        const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-        const int epc = (a.E + size - 1) / size, e_hi = min(a.E, (rank + 1) * epc);
-        auto put = [&](int t, int e, float v) {
-            for (int r = 0; r < size; ++r) *cluster.map_shared_rank(&s_logit[t][e], r) = v;
-        };
-        if (size > 1) cluster.sync();  // every CTA of the cluster has started
-        if (a.lslices > 0) {
-            for (int i = tid; i < T * (e_hi - rank * epc); i += kFewThreads) {
-                const int t = i / (e_hi - rank * epc), e = rank * epc + i % (e_hi - rank * epc);
+    if (a.lslices > 0) {
+        for (int t = 0; t < T; ++t)
+            for (int i = e_lo + tid; i < e_hi; i += kFewThreads) {
                 float v = 0.f;
-                for (int s = 0; s < a.lslices; ++s) v += __ldcg(a.lpart + ((size_t)s * T + t) * a.E + e);
-                put(t, e, v);
+                for (int s = 0; s < a.lslices; ++s) v += __ldcg(a.lpart + ((size_t)s * T + t) * a.E + i);
+                for (int c = 0; c < size; ++c) *cluster.map_shared_rank(&s_logit[t][i], c) = v;
             }
-        } else {
-            for (int e = rank * epc + warp; e < e_hi; e += kFewWarps) {
-                float acc[kFewTok] = {};
-                const float4* w = reinterpret_cast<const float4*>(a.rw + (size_t)e * H) + lane;
-                const uint2* x = reinterpret_cast<const uint2*>(a.x) + lane;
-                for (int b = 0; b < H / 128; b += 4) {
-                    float4 wv[4];
+    } else {
+        float acc[kFewTok] = {};
+        for (int b = 0; e < e_hi;) {
+            float4 w[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        wv[i] = b + i < H / 128 ? __ldg(w + (b + i) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < 8; ++i) w[i] = wn[i];
+            const int e_now = e, b_now = b;
+            b += 8;
+            const bool last = b >= H / 128;
+            if (last) {
+                b = 0;
+                e += kFewWarps;
+            }
+            if (e < e_hi) load_w(e, b);
+            const int nb = min(8, H / 128 - b_now);
 #pragma unroll
-                    for (int t = 0; t < kFewTok; ++t) {
-                        if (t >= T) break;
+            for (int t = 0; t < kFewTok; ++t) {
+                if (t >= T) break;
+                const uint2* xt = reinterpret_cast<const uint2*>(x + (size_t)t * H + b_now * 128) + lane;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (b + i >= H / 128) break;
-                            const uint2 xv = __ldg(x + (size_t)t * (H / 4) + (b + i) * 32);
-                            acc[t] = fmaf(bf16lo(xv.x), wv[i].x, acc[t]);
-                            acc[t] = fmaf(bf16hi(xv.x), wv[i].y, acc[t]);
-                            acc[t] = fmaf(bf16lo(xv.y), wv[i].z, acc[t]);
-                            acc[t] = fmaf(bf16hi(xv.y), wv[i].w, acc[t]);
-                        }
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    if (i >= nb) break;
+                    const uint2 xv = xt[i * 32];
+                    acc[t] = fmaf(bf16lo(xv.x), w[i].x, acc[t]);
+                    acc[t] = fmaf(bf16hi(xv.x), w[i].y, acc[t]);
+                    acc[t] = fmaf(bf16lo(xv.y), w[i].z, acc[t]);
+                    acc[t] = fmaf(bf16hi(xv.y), w[i].w, acc[t]);
                 }
+            }
+            if (!last) continue;
 #pragma unroll
-                for (int t = 0; t < kFewTok; ++t) {
-                    if (t >= T) break;
-                    float v = acc[t];
-                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    if (lane < size) *cluster.map_shared_rank(&s_logit[t][e], lane) = v;
-                }
+            for (int t = 0; t < kFewTok; ++t) {
+                if (t >= T) break;
+                float v = acc[t];
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane < size) *cluster.map_shared_rank(&s_logit[t][e_now], lane) = v;
+                acc[t] = 0.f;
             }
         }
     }
 
     // int8 activations, while the cluster's other logits arrive
-    quantize_tokens<kCoarse>(a.x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
-    if (cluster.num_blocks() > 1) cluster.sync();
+    quantize_tokens<kCoarse>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
+    if (size > 1) cluster.sync();
     else __syncthreads();
 
-    if (warp < T) {
-        int e;
-        float w;
-        few_select(a, s_logit[warp], lane, e, w);
-        if (lane < a.K) {
-            const int i = warp * a.K + lane;
-            s_e[i] = e;
-            s_w[i] = w;
-            if (blockIdx.x == 0) {
-                a.idx[i] = e;
-                if (a.topk_idx_out) a.topk_idx_out[i] = e;
-                if (a.topk_w_out) a.topk_w_out[i] = w;
-            }
-        }
+    // Scores (two warps a token, rolled: this code runs once a launch and is
+    // fetched cold), the picks (a warp a token), the tables.
+    if ((warp & 7) < T) {
+        float* s = s_logit[warp & 7];
+#pragma unroll 1
+        for (int i = (warp >> 3) * 32 + lane; i < a.E; i += 64) s[i] = 1.0f / (1.0f + expf(-s[i]));
     }
     __syncthreads();
-    few_gather(P, T, a.K, tid < T * a.K ? s_e[tid] : -1, tid < T * a.K ? s_w[tid] : 0.f);
+    int my_e = -1;
+    float my_w = 0.f;
+    if (warp < T) {
+        few_select(a, s_logit[warp], s_bias, lane, my_e, my_w);
+        if (lane < a.K) {
+            if (my_e >= 0) atomicOr(&s_mask[my_e >> 5], 1u << (my_e & 31));
+            if (blockIdx.x == 0) {
+                const int i = warp * a.K + lane;
+                if (a.topk_idx_out) a.topk_idx_out[i] = my_e;
+                if (a.topk_w_out) a.topk_w_out[i] = my_w;
+            }
+        }
+        if (lane >= a.K) my_e = -1;
+    }
+    __syncthreads();
+    if (my_e >= 0) {
+        int u = __popc(s_mask[my_e >> 5] & ((1u << (my_e & 31)) - 1));
+        for (int i = 0; i < (my_e >> 5); ++i) u += __popc(s_mask[i]);
+        P.expert[u] = my_e;
+        P.slot[u][warp] = (int8_t)(warp * a.K + lane);
+        s_weight[u][warp] = my_w;
+        atomicOr(&P.tokens[u], 1u << warp);
+    }
+    if (tid == kFewThreads - 1) {
+        int n = 0;
+        for (int i = 0; i < kMaxE / 32; ++i) n += __popc(s_mask[i]);
+        P.U = n;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int i = tid; i < (int)(sizeof(FewPicks) / 4); i += kFewThreads)
+            reinterpret_cast<int*>(a.picks)[i] = reinterpret_cast<const int*>(&P)[i];
     {  // the routed tiles are known now: fill the ring
         const bool was = it < known;
         known = shared_tiles + P.U * expert_tiles;
@@ -364,13 +366,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
                 uv += o[8];
             }
             float h = silu_mul(gv, uv);
-            if (t.u >= 0) h *= P.weight[t.u][warp];
+            if (t.u >= 0) h *= s_weight[t.u][warp];
             const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
             // block_scale of the magnitude rounded up to bf16's seven bits
             float s, inv;
             block_scale((m >> 16) + ((m & 0xffffu) != 0), &s, &inv);
             const uint32_t f = fixed16(h, inv);
-            const int at = t.i0 + (lane & ~7) + ((lane & 1) << 2) + ((lane & 7) >> 1);  // order of lo8 / hi8
+            // eight columns in the order of lo8 / hi8; the eights of two blocks side by side (a lane's 16 bytes)
+            const int at = (t.i0 & ~63) + (lane >> 3) * 16 + ((t.i0 >> 5) & 1) * 8 + ((lane & 1) << 2) + ((lane & 7) >> 1);
             const size_t base = t.u < 0 ? (size_t)T * a.K * 2 * a.I + (size_t)warp * 2 * a.Is
                                         : (size_t)P.slot[t.u][warp] * 2 * a.I;
             a.hq[base + at] = (int8_t)((f + 128) >> 8);
@@ -386,8 +389,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
 // One staged chunk of w2 times one tile of four tokens, block by block of 32
 // columns, each with the token's own scale hv[b] beside the row's.
 template <bool kCoarse>
-__device__ __forceinline__ void down_mma(uint32_t stage, const uint2 (&x)[8], const float (&hv)[8], const float (&sc)[4],
+__device__ __forceinline__ void down_mma(uint32_t stage, const uint4 (&x)[4], const float4 (&h4)[2], const float (&sc)[4],
                                          int gshift, int lane, float (&t)[2]) {
+    const float hv[8] = {h4[0].x, h4[0].y, h4[0].z, h4[0].w, h4[1].x, h4[1].y, h4[1].z, h4[1].w};
     const int g = lane >> 2, q = lane & 3, quad = lane & 28;
     const uint32_t row = stage + g * 128 + (seg_perm(g) << 4) + q * 4;
     t[0] = t[1] = 0.f;
@@ -397,7 +401,7 @@ __device__ __forceinline__ void down_mma(uint32_t stage, const uint2 (&x)[8], co
         const uint32_t wa = lds32(at), wb = lds32(at + 1024);
         const uint32_t a[4] = {lo8(wa), lo8(wb), hi8(wa), hi8(wb)};
         int d[4];
-        mma_s8_first(d, a, x[b].x, x[b].y);
+        mma_s8_first(d, a, (b & 1) ? x[b >> 1].z : x[b >> 1].x, (b & 1) ? x[b >> 1].w : x[b >> 1].y);
         const bool fine = !kCoarse && gshift == 5;
         const int from = quad | (kCoarse ? b >> 2 : fine ? b & 3 : b >> 1);
         const float s0 = __shfl_sync(0xffffffffu, fine ? sc[b >> 2] : sc[0], from);
@@ -408,7 +412,8 @@ __device__ __forceinline__ void down_mma(uint32_t stage, const uint2 (&x)[8], co
 }
 
 // Down projection of whole output tiles: 16 rows, the shared expert and all
-// touched ones as one long sum, its chunks dealt out to the CTA's warps.
+// touched ones as one long sum, its chunks (units) dealt out to the CTA's
+// warps: unit v to warp v mod 16, the shared expert's chunks first.
 template <int NT, bool kCoarse>
 __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -421,27 +426,61 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
     const uint32_t ring = smem_addr(smem + warp * (kFewDepth * kStageBytes));
     const int Cs = (a.Is + kChunkK - 1) / kChunkK, Ci = (a.I + kChunkK - 1) / kChunkK;
     const int tiles = a.H / 16;
-    int units = Cs;  // (expert, chunk) pairs of a tile, as far as they are known: the shared expert's first
+    int units = Cs;  // units of a tile, as far as they are known
     bool all = false;
 
-    int it = blockIdx.x, iv = warp, ahead = 0;  // next copy; stages filled before the picks are known
+    // Unit v as (expert u or -1, chunk c); 16 units on, 16 / Ci experts and 16 % Ci chunks.
+    struct At {
+        int v, u, c;
+    };
+    const int du = kFewWarps / Ci, dc = kFewWarps % Ci;
+    auto routed = [&](At& p) {
+        p.u = (p.v - Cs) / Ci;
+        p.c = p.v - Cs - p.u * Ci;
+    };
+    auto first = [&]() {
+        At p = {warp, -1, warp};
+        if (warp >= Cs) routed(p);
+        return p;
+    };
+    auto step = [&](At& p) {
+        p.v += kFewWarps;
+        if (p.u >= 0) {
+            p.u += du;
+            p.c += dc;
+            if (p.c >= Ci) {
+                p.c -= Ci;
+                ++p.u;
+            }
+        } else if (p.v >= Cs) {
+            routed(p);
+        } else {
+            p.c = p.v;
+        }
+    };
+    const size_t e_bytes = (size_t)a.H * (a.I / 2), e_scales = (size_t)a.H * a.G2;
+    const int lane_r = (lane >> 3) * (a.I / 2) + (lane & 7) * 16, lane_s = (lane >> 3) * (a.Is / 2) + (lane & 7) * 16;
+
+    At ia = first();  // next copy
+    int it = blockIdx.x, ahead = 0;  // its tile; stages filled before the picks are known
     uint32_t dst = ring + stage_at(lane);
     const uint32_t dst_end = dst + kFewDepth * kStageBytes;
     auto issue = [&]() {
-        if (it < tiles && iv < units) {
-            const bool sh = iv < Cs;
-            const int u = sh ? 0 : (iv - Cs) / Ci, c = sh ? iv : iv - Cs - u * Ci, I = sh ? a.Is : a.I;
-            const uint8_t* w = sh ? a.sh_w2 : a.w2 + (size_t)P.expert[u] * a.H * (I / 2);
+        if (it < tiles && ia.v < units) {
+            const bool sh = ia.u < 0;
+            const int half = (sh ? a.Is : a.I) / 2;
+            const uint8_t* w = sh ? a.sh_w2 + lane_s : a.w2 + P.expert[ia.u] * e_bytes + lane_r;
             const uint8_t* ip[4];
+            ip[0] = w + (size_t)(it * 16) * half;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ip[i] = w + (size_t)(it * 16 + (lane >> 3) + 4 * i) * (I / 2) + (lane & 7) * 16;
-            issue_chunk(dst, ip, c, c * kChunkK + (lane & 7) * 32 < I);
+            for (int i = 1; i < 4; ++i) ip[i] = ip[i - 1] + 4 * half;
+            issue_chunk(dst, ip, ia.c, ia.c * kChunkK + (lane & 7) * 32 < 2 * half);
             dst += kStageBytes;
             if (dst == dst_end) dst -= kFewDepth * kStageBytes;
             ++ahead;
-            iv += kFewWarps;
-            if (all && iv >= units) {
-                iv = warp;
+            step(ia);
+            if (all && ia.v >= units) {
+                ia = first();
                 it += gridDim.x;
             }
         }
@@ -451,88 +490,79 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
 
     pdl_wait();
     pdl_release();
-    few_gather(P, T, a.K, tid < T * a.K ? __ldcg(a.idx + tid) : -1, 0.f);
+    for (int i = tid; i < (int)(sizeof(FewPicks) / 4); i += kFewThreads)
+        reinterpret_cast<int*>(&P)[i] = __ldcg(reinterpret_cast<const int*>(a.picks) + i);
+    __syncthreads();
     units = Cs + P.U * Ci;
     all = true;
-    if (iv >= units && warp < units) {
-        iv = warp;
+    if (ia.v >= units && warp < units) {
+        ia = first();
         it += gridDim.x;
     }
     for (int i = ahead; i < kFewDepth; ++i) issue();  // see few_gate_up_kernel
 
-    const size_t hq_shared = (size_t)T * a.K * 2 * a.I;
-    const int hs_shared = T * a.K * a.I;
+    const int8_t* hq_shared = a.hq + (size_t)T * a.K * 2 * a.I;
+    const float* hs_shared = a.hs + T * a.K * a.I / 32;
     int slot = 0, parity = 0;
-    // A unit's row scales and its first tile of tokens are loaded one unit ahead.
-    struct Unit {
-        bool sh;
-        int u, c, I, blocks;
-        unsigned tokens;
-    };
-    auto unit = [&](int v) {
-        Unit t;
-        t.sh = v < Cs;
-        t.u = t.sh ? 0 : (v - Cs) / Ci;
-        t.c = t.sh ? v : v - Cs - t.u * Ci;
-        t.I = t.sh ? a.Is : a.I;
-        t.blocks = min(8, (t.I - t.c * kChunkK) / 32);  // 4 or 8
-        t.tokens = t.sh ? (1u << T) - 1 : P.tokens[t.u];
-        return t;
-    };
-    auto load_scales = [&](const Unit& t, int i, float (&sc)[4]) {
-        const size_t row = (t.sh ? 0 : (size_t)P.expert[t.u] * a.H) + (size_t)i * 16;
-        const int G = t.sh ? a.Gs2 : a.G2;
+    auto tokens_of = [&](const At& p) { return p.u < 0 ? (1u << T) - 1 : P.tokens[p.u]; };
+    auto load_scales = [&](const At& p, int i, float (&sc)[4]) {
+        const int G = p.u < 0 ? a.Gs2 : a.G2, sh = a.stype == kScaleF32 ? 2 : 1;
         ScaleRows sr;
-        sr.open(t.sh ? a.sh_s2 : a.s2, row + g, row + g + 8, G, a.stype);
-        load_chunk_scales<kCoarse>(sc, sr, t.c, a.gshift, G, a.stype, q);
+        sr.p0 = static_cast<const char*>(p.u < 0 ? a.sh_s2 : a.s2) + (((p.u < 0 ? 0 : P.expert[p.u] * e_scales) + (size_t)(i * 16 + g) * G) << sh);
+        sr.p8 = sr.p0 + ((8 * G) << sh);
+        load_chunk_scales<kCoarse>(sc, sr, p.c, a.gshift, G, a.stype, q);
     };
     // This lane's B row (token 4 n + g / 2, part g % 2) and the block scales of
     // its D columns (token 4 n + q); zero for a token that did not pick the expert.
-    auto load_h = [&](const Unit& t, int n, uint2 (&x)[8], float (&hv)[8]) {
+    auto load_h = [&](const At& p, unsigned tokens, int n, uint4 (&x)[4], float4 (&hv)[2]) {
         const int tb = 4 * n + (g >> 1), td = 4 * n + q;
-        const bool hb = (t.tokens >> tb) & 1u, hd = (t.tokens >> td) & 1u;
-        const int sb = t.sh ? tb : P.slot[t.u][tb], sd = t.sh ? td : P.slot[t.u][td];
-        const uint2* xp = reinterpret_cast<const uint2*>(a.hq + (t.sh ? hq_shared : 0) + (size_t)(2 * max(sb, 0) + (g & 1)) * t.I +
-                                                         t.c * kChunkK) + q;
-        const float4* hp = reinterpret_cast<const float4*>(a.hs + ((t.sh ? hs_shared : 0) + max(sd, 0) * t.I + t.c * kChunkK) / 32);
+        const int I = p.u < 0 ? a.Is : a.I, left = I - p.c * kChunkK;
+        const bool hb = (tokens >> tb) & 1u, hd = (tokens >> td) & 1u;
+        const int sb = p.u < 0 ? tb : P.slot[p.u][tb], sd = p.u < 0 ? td : P.slot[p.u][td];
+        const uint4* xp = reinterpret_cast<const uint4*>((p.u < 0 ? hq_shared : a.hq) + (2 * sb + (g & 1)) * I + p.c * kChunkK) + q;
+        const float4* hp = reinterpret_cast<const float4*>((p.u < 0 ? hs_shared : a.hs) + (sd * I + p.c * kChunkK) / 32);
 #pragma unroll
-        for (int b = 0; b < 8; ++b) x[b] = hb && b < t.blocks ? __ldcg(xp + 4 * b) : make_uint2(0, 0);
+        for (int b = 0; b < 4; ++b) x[b] = hb && 64 * b < left ? __ldcg(xp + 4 * b) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const float4 f = hd && 4 * b < t.blocks ? __ldcg(hp + b) : make_float4(0.f, 0.f, 0.f, 0.f);
-            hv[4 * b] = f.x;
-            hv[4 * b + 1] = f.y;
-            hv[4 * b + 2] = f.z;
-            hv[4 * b + 3] = f.w;
-        }
+        for (int b = 0; b < 2; ++b) hv[b] = hd && 128 * b < left ? __ldcg(hp + b) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    auto first_n = [&](const Unit& t) { return NT > 1 && !(t.tokens & 15u) ? 1 : 0; };
-    float nsc[4], nhv[8];
-    uint2 nx[8];
-    Unit next;
+    auto first_n = [&](unsigned tokens) { return NT > 1 && !(tokens & 15u) ? 1 : 0; };
+    // A unit's row scales and its first tile of tokens are loaded one unit ahead.
+    float nsc[4];
+    float4 nhv[2];
+    uint4 nx[4];
+    At na = first();
+    unsigned ntok = 0;
     if (warp < units && (int)blockIdx.x < tiles) {
-        next = unit(warp);
-        load_scales(next, blockIdx.x, nsc);
-        load_h(next, first_n(next), nx, nhv);
+        ntok = tokens_of(na);
+        load_scales(na, blockIdx.x, nsc);
+        load_h(na, ntok, first_n(ntok), nx, nhv);
     }
     for (int i = blockIdx.x; i < tiles; i += gridDim.x, parity ^= 1) {
         float acc[NT][2] = {};
         for (int v = warp; v < units; v += kFewWarps) {
-            const Unit now = next;
-            float sc[4], hv[8];
-            uint2 x[8];
+            const At now = na;
+            const unsigned tokens = ntok;
+            float sc[4];
+            float4 hv[2];
+            uint4 x[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) sc[u] = nsc[u];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                hv[u] = nhv[u];
+            for (int u = 0; u < 4; ++u) {
+                sc[u] = nsc[u];
                 x[u] = nx[u];
             }
-            const bool more = v + kFewWarps < units;
-            if (more || i + (int)gridDim.x < tiles) {
-                next = unit(more ? v + kFewWarps : warp);
-                load_scales(next, more ? i : i + gridDim.x, nsc);
-                load_h(next, first_n(next), nx, nhv);
+            hv[0] = nhv[0];
+            hv[1] = nhv[1];
+            step(na);
+            int ni = i;
+            if (na.v >= units) {
+                na = first();
+                ni += gridDim.x;
+            }
+            if (ni < tiles) {
+                ntok = tokens_of(na);
+                load_scales(na, ni, nsc);
+                load_h(na, ntok, first_n(ntok), nx, nhv);
             }
             scale_values(sc, a.stype);
             cp_async_wait<kFewDepth - 1>();
@@ -541,11 +571,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
             slot = slot == kFewDepth - 1 ? 0 : slot + 1;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if (NT > 1 && !((now.tokens >> (4 * n)) & 15u)) continue;
-                if (NT > 1 && n != first_n(now)) load_h(now, n, x, hv);
+                if (NT > 1 && !((tokens >> (4 * n)) & 15u)) continue;
+                if (NT > 1 && n != first_n(tokens)) load_h(now, tokens, n, x, hv);
                 float t[2];
                 down_mma<kCoarse>(st, x, hv, sc, a.gshift, lane, t);
-                if ((now.tokens >> (4 * n + q)) & 1u) {
+                if ((tokens >> (4 * n + q)) & 1u) {
                     acc[n][0] += t[0];
                     acc[n][1] += t[1];
                 }
@@ -563,11 +593,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
         __syncthreads();
         if (tid < 16 * T) {
             const int r = tid & 15, t = tid >> 4;
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kFewWarps; ++w) v += part[(w * 4 * NT + t) * 16 + r];
             const size_t o = (size_t)t * a.H + i * 16 + r;
-            if (a.flags & kFlagResidual) v += __bfloat162float(a.x[o]);
+            float v = a.flags & kFlagResidual ? __bfloat162float(a.x[o]) : 0.f;
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFewWarps; ++w) y += part[(w * 4 * NT + t) * 16 + r];
+            v += y;
             if (a.flags & kFlagOutF32) static_cast<float*>(a.out)[o] = v;
             else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
         }
@@ -624,7 +655,7 @@ cudaError_t few_launch(const FewArgs& a, cudaStream_t stream) {
     if (d.clustered == 0) {
         int n = 0, sms = 0;
         // static shared memory comes on top of the dynamic part
-        constexpr int kMax = kFewSmemMax - 12 * 1024;
+        constexpr int kMax = kFewSmemMax - 13 * 1024;
         e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
         if (e == cudaSuccess) e = few_launch_cluster(up, kFewCluster, kFewCluster, kMax, nullptr, a, &n);
@@ -665,7 +696,7 @@ size_t few_workspace(FewArgs& a, void* ws) {
         return p;
     };
     const size_t TK = (size_t)a.T * a.K, n = TK * a.I + (size_t)a.T * a.Is;
-    a.idx = reinterpret_cast<int32_t*>(take(TK * 4));
+    a.picks = reinterpret_cast<FewPicks*>(take(sizeof(FewPicks)));
     a.hq = reinterpret_cast<int8_t*>(take(2 * n));
     a.hs = reinterpret_cast<float*>(take(n / 32 * 4));
     a.lslices = few_split_router(a.E, a.H) ? few_logit_slices(a.H) : 0;

@@ -27,6 +27,16 @@ struct LinearArgs {
     long long ldx, ldo, lda;
 };
 
+// What the picks of a pass of the few-token layer come to.
+constexpr int kFewTok = 8;  // tokens of a pass at most
+constexpr int kFewMaxU = kFewTok * kMaxK;
+struct FewPicks {
+    int U;                           // touched experts
+    int expert[kFewMaxU];            // ascending
+    unsigned tokens[kFewMaxU];       // bit t: token t picked it
+    int8_t slot[kFewMaxU][kFewTok];  // t * K + k of token t's pick of the expert, or -1
+};
+
 struct FewArgs {
     const __nv_bfloat16* x;
     const float* rw;
@@ -42,7 +52,7 @@ struct FewArgs {
     int gshift, stype;
     int G13, G2, Gs2;  // scales per row of w13 (and sh_w13), w2, sh_w2
     // workspace
-    int32_t* idx;  // [T][K] picks (-1: dropped)
+    FewPicks* picks;
     int8_t* hq;    // [T*K][2][I] then [T][2][Is]: both int8 parts of h
     float* hs;     // [T*K][I/32] then [T][Is/32]: their scales
     float* lpart;  // [lslices][T][E] partial router logits (lslices = 0: none)

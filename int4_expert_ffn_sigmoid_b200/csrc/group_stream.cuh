@@ -120,7 +120,7 @@ __device__ __forceinline__ void quantize_tokens(const __nv_bfloat16* x, long lon
             t[u] = i / chunks;
             c[u] = i - t[u] * chunks;
             const int k = c[u] * kChunkK + 8 * lane;
-            v[u] = t[u] < nt && k < K ? __ldg(reinterpret_cast<const uint4*>(x + t[u] * ldx + k)) : make_uint4(0, 0, 0, 0);
+            v[u] = t[u] < nt && k < K ? *reinterpret_cast<const uint4*>(x + t[u] * ldx + k) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
