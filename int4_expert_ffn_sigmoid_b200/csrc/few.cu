@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     if (tid < a.E) s_bias[tid] = __ldg(a.rb + tid);
     if (tid < kMaxE / 32) s_mask[tid] = 0;
     if (tid < kFewMaxU) P.tokens[tid] = 0;
-    P.slot[tid / kFewTok][tid % kFewTok] = -1;
-    static_assert(kFewThreads == kFewMaxU * kFewTok, "one slot a thread");
+    if (tid < kFewMaxU * kFewTok) P.slot[tid / kFewTok][tid % kFewTok] = -1;
+    static_assert(kFewThreads >= kFewMaxU * kFewTok, "one slot a thread");
     // The dot product of this warp's experts e_lo + warp, + 16, ...: eight
     // 128-column blocks of weights at a time, the next ones on their way.
     float4 wn[8];
@@ -186,12 +186,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     };
     int e = a.lslices > 0 ? e_hi : e_lo + warp;
     if (e < e_hi) load_w(e, 0);
+    // Behind the logits kernel x is final: that kernel let this one start only
+    // after its own wait for whatever wrote x.
+    if (a.lslices > 0)
+        quantize_tokens<kCoarse>(a.x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
     pdl_wait();
     pdl_release();
 
     // x in shared memory where it fits the room of the partial sums
     const __nv_bfloat16* x = a.x;
-    if ((size_t)T * H * 2 <= 2 * kRed * 4) {
+    if (a.lslices == 0 && (size_t)T * H * 2 <= 2 * kRed * 4) {
         __nv_bfloat16* xr = reinterpret_cast<__nv_bfloat16*>(red);
         for (int i = tid; i < T * H / 8; i += kFewThreads)
             reinterpret_cast<uint4*>(xr)[i] = __ldg(reinterpret_cast<const uint4*>(a.x) + i);
@@ -202,12 +206,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
 
     // Router logits of this CTA's experts, to every CTA of the cluster.
     if (a.lslices > 0) {
-        for (int t = 0; t < T; ++t)
-            for (int i = e_lo + tid; i < e_hi; i += kFewThreads) {
-                float v = 0.f;
-                for (int s = 0; s < a.lslices; ++s) v += __ldcg(a.lpart + ((size_t)s * T + t) * a.E + i);
-                for (int c = 0; c < size; ++c) *cluster.map_shared_rank(&s_logit[t][i], c) = v;
-            }
+        for (int i = tid; i < T * a.E; i += kFewThreads) {  // no cluster then: every CTA sums all of them
+            const float* l = a.lpart + i;
+            float v = 0.f;
+#pragma unroll 8
+            for (int s = 0; s < a.lslices; ++s) v += __ldcg(l + (size_t)s * T * a.E);
+            s_logit[i / a.E][i % a.E] = v;
+        }
     } else {
         float acc[kFewTok] = {};
         for (int b = 0; e < e_hi;) {
@@ -250,7 +255,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     }
 
     // int8 activations, while the cluster's other logits arrive
-    quantize_tokens<kCoarse>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
+    if (a.lslices == 0)
+        quantize_tokens<kCoarse>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
     if (size > 1) cluster.sync();
     else __syncthreads();
 
@@ -302,6 +308,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         // n-th stage is then never among the last kFewDepth - 1 when it is read.
         for (int i = ahead; i < kFewDepth; ++i) issue();
     }
+    // With its last copy issued, the CTA brings what the down kernel's CTA of
+    // the same index reads first (a ring's worth of routed units) into L2.
+    bool last_issued = false;
+    auto prefetch_down = [&]() {
+        if (last_issued || it < known) return;
+        last_issued = true;
+        const int Cs = (a.Is + kChunkK - 1) / kChunkK, Ci = (a.I + kChunkK - 1) / kChunkK;
+        if ((int)blockIdx.x >= H / 16 || lane >= 16) return;
+        for (int i = 0; i < kFewDepth; ++i) {
+            const int v = warp + i * kFewWarps - Cs;
+            if (v < 0 || v >= P.U * Ci) continue;
+            const size_t row = (size_t)P.expert[v / Ci] * H + blockIdx.x * 16 + lane;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.w2 + row * (a.I / 2) + v % Ci * (kChunkK / 2)));
+        }
+    };
+    prefetch_down();
 
     uint32_t xrow[NT];
     const float* xsc[NT];
@@ -348,6 +370,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
             }
             __syncwarp();
             issue();
+            prefetch_down();
         }
         float* part = red + parity * kRed;
 #pragma unroll
@@ -386,14 +409,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     cp_async_wait<0>();
 }
 
-// One staged chunk of w2 times one tile of four tokens, block by block of 32
-// columns, each with the token's own scale hv[b] beside the row's.
+// One staged chunk of w2 times one tile of four tokens: a block of 32 columns
+// at a time, its sum times the token's own scale of the block (hv), the blocks
+// of a scale group together times the rows' scales.
 template <bool kCoarse>
 __device__ __forceinline__ void down_mma(uint32_t stage, const uint4 (&x)[4], const float4 (&h4)[2], const float (&sc)[4],
                                          int gshift, int lane, float (&t)[2]) {
     const float hv[8] = {h4[0].x, h4[0].y, h4[0].z, h4[0].w, h4[1].x, h4[1].y, h4[1].z, h4[1].w};
     const int g = lane >> 2, q = lane & 3, quad = lane & 28;
     const uint32_t row = stage + g * 128 + (seg_perm(g) << 4) + q * 4;
+    float u0 = 0.f, u8 = 0.f;
     t[0] = t[1] = 0.f;
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
@@ -402,14 +427,24 @@ __device__ __forceinline__ void down_mma(uint32_t stage, const uint4 (&x)[4], co
         const uint32_t a[4] = {lo8(wa), lo8(wb), hi8(wa), hi8(wb)};
         int d[4];
         mma_s8_first(d, a, (b & 1) ? x[b >> 1].z : x[b >> 1].x, (b & 1) ? x[b >> 1].w : x[b >> 1].y);
+        u0 = fmaf((float)(d[0] * 256 + d[1]), hv[b], u0);
+        u8 = fmaf((float)(d[2] * 256 + d[3]), hv[b], u8);
         const bool fine = !kCoarse && gshift == 5;
-        const int from = quad | (kCoarse ? b >> 2 : fine ? b & 3 : b >> 1);
-        const float s0 = __shfl_sync(0xffffffffu, fine ? sc[b >> 2] : sc[0], from);
-        const float s8 = __shfl_sync(0xffffffffu, fine ? sc[2 + (b >> 2)] : sc[2], from);
-        t[0] = fmaf((float)(d[0] * 256 + d[1]), s0 * hv[b], t[0]);
-        t[1] = fmaf((float)(d[2] * 256 + d[3]), s8 * hv[b], t[1]);
+        if (kCoarse ? (b & 3) == 3 : fine || (b & 1)) {
+            const int from = quad | (kCoarse ? b >> 2 : fine ? b & 3 : b >> 1);
+            t[0] = fmaf(u0, __shfl_sync(0xffffffffu, fine ? sc[b >> 2] : sc[0], from), t[0]);
+            t[1] = fmaf(u8, __shfl_sync(0xffffffffu, fine ? sc[2 + (b >> 2)] : sc[2], from), t[1]);
+            u0 = u8 = 0.f;
+        }
     }
 }
+
+struct alignas(16) Unit {
+    const uint8_t* w;
+    const char* s;
+    int u, c, I, G;
+    unsigned tokens;
+};
 
 // Down projection of whole output tiles: 16 rows, the shared expert and all
 // touched ones as one long sum, its chunks (units) dealt out to the CTA's
@@ -429,58 +464,45 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
     int units = Cs;  // units of a tile, as far as they are known
     bool all = false;
 
-    // Unit v as (expert u or -1, chunk c); 16 units on, 16 / Ci experts and 16 % Ci chunks.
-    struct At {
-        int v, u, c;
+    // Where unit v is, worked out once for all tiles: the byte of its first
+    // code in the first row of w2 (or sh_w2), its first scale, the columns of
+    // its row, its h, the tokens.  [units], behind the partial sums.
+    Unit* list = reinterpret_cast<Unit*>(red + 2 * kRed);
+    auto describe = [&](int v) {
+        Unit d;
+        const bool sh = v < Cs;
+        const int u = sh ? -1 : (v - Cs) / Ci, c = sh ? v : v - Cs - u * Ci;
+        const size_t row = sh ? 0 : (size_t)P.expert[u] * a.H;
+        d.I = sh ? a.Is : a.I;
+        d.G = sh ? a.Gs2 : a.G2;
+        d.w = (sh ? a.sh_w2 : a.w2) + row * (d.I / 2) + c * (kChunkK / 2);
+        d.s = static_cast<const char*>(sh ? a.sh_s2 : a.s2) + ((row * d.G) << (a.stype == kScaleF32 ? 2 : 1));
+        d.u = u;
+        d.c = c;
+        d.tokens = sh ? (1u << T) - 1 : P.tokens[u];
+        return d;
     };
-    const int du = kFewWarps / Ci, dc = kFewWarps % Ci;
-    auto routed = [&](At& p) {
-        p.u = (p.v - Cs) / Ci;
-        p.c = p.v - Cs - p.u * Ci;
-    };
-    auto first = [&]() {
-        At p = {warp, -1, warp};
-        if (warp >= Cs) routed(p);
-        return p;
-    };
-    auto step = [&](At& p) {
-        p.v += kFewWarps;
-        if (p.u >= 0) {
-            p.u += du;
-            p.c += dc;
-            if (p.c >= Ci) {
-                p.c -= Ci;
-                ++p.u;
-            }
-        } else if (p.v >= Cs) {
-            routed(p);
-        } else {
-            p.c = p.v;
-        }
-    };
-    const size_t e_bytes = (size_t)a.H * (a.I / 2), e_scales = (size_t)a.H * a.G2;
-    const int lane_r = (lane >> 3) * (a.I / 2) + (lane & 7) * 16, lane_s = (lane >> 3) * (a.Is / 2) + (lane & 7) * 16;
+    for (int v = tid; v < Cs; v += kFewThreads) list[v] = describe(v);
+    __syncthreads();
 
-    At ia = first();  // next copy
-    int it = blockIdx.x, ahead = 0;  // its tile; stages filled before the picks are known
+    int iv = warp, it = blockIdx.x, ahead = 0;  // next copy: unit and tile; stages filled before the picks are known
     uint32_t dst = ring + stage_at(lane);
     const uint32_t dst_end = dst + kFewDepth * kStageBytes;
     auto issue = [&]() {
-        if (it < tiles && ia.v < units) {
-            const bool sh = ia.u < 0;
-            const int half = (sh ? a.Is : a.I) / 2;
-            const uint8_t* w = sh ? a.sh_w2 + lane_s : a.w2 + P.expert[ia.u] * e_bytes + lane_r;
+        if (it < tiles && iv < units) {
+            const Unit& d = list[iv];
+            const int half = d.I / 2;
             const uint8_t* ip[4];
-            ip[0] = w + (size_t)(it * 16) * half;
+            ip[0] = d.w + (size_t)(it * 16 + (lane >> 3)) * half + (lane & 7) * 16;
 #pragma unroll
             for (int i = 1; i < 4; ++i) ip[i] = ip[i - 1] + 4 * half;
-            issue_chunk(dst, ip, ia.c, ia.c * kChunkK + (lane & 7) * 32 < 2 * half);
+            issue_chunk(dst, ip, 0, d.c * kChunkK + (lane & 7) * 32 < d.I);
             dst += kStageBytes;
             if (dst == dst_end) dst -= kFewDepth * kStageBytes;
             ++ahead;
-            step(ia);
-            if (all && ia.v >= units) {
-                ia = first();
+            iv += kFewWarps;
+            if (all && iv >= units) {
+                iv = warp;
                 it += gridDim.x;
             }
         }
@@ -494,9 +516,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
         reinterpret_cast<int*>(&P)[i] = __ldcg(reinterpret_cast<const int*>(a.picks) + i);
     __syncthreads();
     units = Cs + P.U * Ci;
+    for (int v = Cs + tid; v < units; v += kFewThreads) list[v] = describe(v);
+    __syncthreads();
     all = true;
-    if (ia.v >= units && warp < units) {
-        ia = first();
+    if (iv >= units && warp < units) {
+        iv = warp;
         it += gridDim.x;
     }
     for (int i = ahead; i < kFewDepth; ++i) issue();  // see few_gate_up_kernel
@@ -504,84 +528,92 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
     const int8_t* hq_shared = a.hq + (size_t)T * a.K * 2 * a.I;
     const float* hs_shared = a.hs + T * a.K * a.I / 32;
     int slot = 0, parity = 0;
-    auto tokens_of = [&](const At& p) { return p.u < 0 ? (1u << T) - 1 : P.tokens[p.u]; };
-    auto load_scales = [&](const At& p, int i, float (&sc)[4]) {
-        const int G = p.u < 0 ? a.Gs2 : a.G2, sh = a.stype == kScaleF32 ? 2 : 1;
-        ScaleRows sr;
-        sr.p0 = static_cast<const char*>(p.u < 0 ? a.sh_s2 : a.s2) + (((p.u < 0 ? 0 : P.expert[p.u] * e_scales) + (size_t)(i * 16 + g) * G) << sh);
-        sr.p8 = sr.p0 + ((8 * G) << sh);
-        load_chunk_scales<kCoarse>(sc, sr, p.c, a.gshift, G, a.stype, q);
+    // What a unit takes besides the staged weights, loaded one unit ahead.
+    struct Operands {
+        float sc[4];
+        uint4 x[4];
+        float4 hv[2];
+        unsigned tokens;
     };
     // This lane's B row (token 4 n + g / 2, part g % 2) and the block scales of
-    // its D columns (token 4 n + q); zero for a token that did not pick the expert.
-    auto load_h = [&](const At& p, unsigned tokens, int n, uint4 (&x)[4], float4 (&hv)[2]) {
-        const int tb = 4 * n + (g >> 1), td = 4 * n + q;
-        const int I = p.u < 0 ? a.Is : a.I, left = I - p.c * kChunkK;
-        const bool hb = (tokens >> tb) & 1u, hd = (tokens >> td) & 1u;
-        const int sb = p.u < 0 ? tb : P.slot[p.u][tb], sd = p.u < 0 ? td : P.slot[p.u][td];
-        const uint4* xp = reinterpret_cast<const uint4*>((p.u < 0 ? hq_shared : a.hq) + (2 * sb + (g & 1)) * I + p.c * kChunkK) + q;
-        const float4* hp = reinterpret_cast<const float4*>((p.u < 0 ? hs_shared : a.hs) + (sd * I + p.c * kChunkK) / 32);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) x[b] = hb && 64 * b < left ? __ldcg(xp + 4 * b) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) hv[b] = hd && 128 * b < left ? __ldcg(hp + b) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // its D columns (token 4 n + q).  A token that did not pick the expert
+    // takes the first that did: its columns' sums are not used.
+    auto load_h = [&](const Unit& d, int n, Operands& o) {
+        const int any = __ffs(o.tokens) - 1;
+        int sb = 4 * n + (g >> 1), sd = 4 * n + q;
+        if (!((o.tokens >> sb) & 1u)) sb = any;
+        if (!((o.tokens >> sd) & 1u)) sd = any;
+        if (d.u >= 0) {
+            sb = P.slot[d.u][sb];
+            sd = P.slot[d.u][sd];
+        }
+        const uint4* xp = reinterpret_cast<const uint4*>((d.u < 0 ? hq_shared : a.hq) + (2 * sb + (g & 1)) * d.I + d.c * kChunkK) + q;
+        const float4* hp = reinterpret_cast<const float4*>((d.u < 0 ? hs_shared : a.hs) + (sd * d.I + d.c * kChunkK) / 32);
+        o.x[0] = __ldcg(xp);
+        o.x[1] = __ldcg(xp + 4);
+        o.hv[0] = __ldcg(hp);
+        if (d.c * kChunkK + 128 < d.I) {
+            o.x[2] = __ldcg(xp + 8);
+            o.x[3] = __ldcg(xp + 12);
+            o.hv[1] = __ldcg(hp + 1);
+        } else {  // half a chunk: the rest of the stage is not its row's
+            o.x[2] = o.x[3] = make_uint4(0, 0, 0, 0);
+            o.hv[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     };
     auto first_n = [&](unsigned tokens) { return NT > 1 && !(tokens & 15u) ? 1 : 0; };
-    // A unit's row scales and its first tile of tokens are loaded one unit ahead.
-    float nsc[4];
-    float4 nhv[2];
-    uint4 nx[4];
-    At na = first();
-    unsigned ntok = 0;
-    if (warp < units && (int)blockIdx.x < tiles) {
-        ntok = tokens_of(na);
-        load_scales(na, blockIdx.x, nsc);
-        load_h(na, ntok, first_n(ntok), nx, nhv);
-    }
+    int nv = warp, ni = blockIdx.x;  // the next unit to load, and its tile
+    const int esh = a.stype == kScaleF32 ? 2 : 1;
+    auto load = [&](Operands& o) {
+        if (nv >= units || ni >= tiles) return;
+        const Unit& d = list[nv];
+        o.tokens = d.tokens;
+        ScaleRows sr;
+        sr.p0 = d.s + (((ni * 16 + g) * d.G) << esh);
+        sr.p8 = sr.p0 + ((8 * d.G) << esh);
+        load_chunk_scales<kCoarse>(o.sc, sr, d.c, a.gshift, d.G, a.stype, q);
+        load_h(d, first_n(o.tokens), o);
+        nv += kFewWarps;
+        if (nv >= units) {
+            nv = warp;
+            ni += gridDim.x;
+        }
+    };
+    float acc[NT][2];
+    auto multiply = [&](Operands& o, int v) {
+        scale_values(o.sc, a.stype);
+        cp_async_wait<kFewDepth - 1>();
+        __syncwarp();
+        const uint32_t st = ring + slot * kStageBytes;
+        slot = slot == kFewDepth - 1 ? 0 : slot + 1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (NT > 1 && !((o.tokens >> (4 * n)) & 15u)) continue;
+            if (NT > 1 && n != first_n(o.tokens)) load_h(list[v], n, o);
+            float t[2];
+            down_mma<kCoarse>(st, o.x, o.hv, o.sc, a.gshift, lane, t);
+            if ((o.tokens >> (4 * n + q)) & 1u) {
+                acc[n][0] += t[0];
+                acc[n][1] += t[1];
+            }
+        }
+        __syncwarp();
+        issue();
+    };
+    Operands A, B;
+    load(A);
     for (int i = blockIdx.x; i < tiles; i += gridDim.x, parity ^= 1) {
-        float acc[NT][2] = {};
-        for (int v = warp; v < units; v += kFewWarps) {
-            const At now = na;
-            const unsigned tokens = ntok;
-            float sc[4];
-            float4 hv[2];
-            uint4 x[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                sc[u] = nsc[u];
-                x[u] = nx[u];
+        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = 0.f;
+        for (int v = warp; v < units; v += 2 * kFewWarps) {  // two at a time: no operand moves between registers
+            load(B);
+            multiply(A, v);
+            if (v + kFewWarps >= units) {
+                A = B;
+                break;
             }
-            hv[0] = nhv[0];
-            hv[1] = nhv[1];
-            step(na);
-            int ni = i;
-            if (na.v >= units) {
-                na = first();
-                ni += gridDim.x;
-            }
-            if (ni < tiles) {
-                ntok = tokens_of(na);
-                load_scales(na, ni, nsc);
-                load_h(na, ntok, first_n(ntok), nx, nhv);
-            }
-            scale_values(sc, a.stype);
-            cp_async_wait<kFewDepth - 1>();
-            __syncwarp();
-            const uint32_t st = ring + slot * kStageBytes;
-            slot = slot == kFewDepth - 1 ? 0 : slot + 1;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (NT > 1 && !((tokens >> (4 * n)) & 15u)) continue;
-                if (NT > 1 && n != first_n(tokens)) load_h(now, tokens, n, x, hv);
-                float t[2];
-                down_mma<kCoarse>(st, x, hv, sc, a.gshift, lane, t);
-                if ((tokens >> (4 * n + q)) & 1u) {
-                    acc[n][0] += t[0];
-                    acc[n][1] += t[1];
-                }
-            }
-            __syncwarp();
-            issue();
+            load(A);
+            multiply(B, v + kFewWarps);
         }
         float* part = red + parity * kRed;
 #pragma unroll
@@ -675,7 +707,10 @@ cudaError_t few_launch(const FewArgs& a, cudaStream_t stream) {
     e = few_launch_cluster(up, grid, cluster, smem, stream, a, nullptr);
     const int out_tiles = a.H / 16;
     if (e == cudaSuccess)
-        e = launch_pdl(down, dim3(out_tiles < d.sms ? out_tiles : d.sms), dim3(kFewThreads), few_smem_base<NT>(), stream, a);
+        e = launch_pdl(down, dim3(out_tiles < d.sms ? out_tiles : d.sms), dim3(kFewThreads),
+                       few_smem_base<NT>() + sizeof(Unit) * ((a.Is + kChunkK - 1) / kChunkK +
+                                                            (size_t)touched * ((a.I + kChunkK - 1) / kChunkK)),
+                       stream, a);
     return e;
 }
 
