@@ -25,6 +25,8 @@ namespace moe {
 constexpr int kFewWarps = 16;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewDepth = 3;
+// The down kernel: more warps, shallower rings.
+constexpr int kDownWarps = 24, kDownThreads = 32 * kDownWarps, kDownDepth = 2;
 constexpr int kFewTileRows = 32;  // h elements of a gate/up tile
 constexpr int kFewSmemMax = 227 * 1024;
 constexpr int kFewXMax = 98 * 1024;
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         last_issued = true;
         const int Cs = (a.Is + kChunkK - 1) / kChunkK, Ci = (a.I + kChunkK - 1) / kChunkK;
         if ((int)blockIdx.x >= H / 16 || lane >= 16) return;
-        for (int i = 0; i < kFewDepth; ++i) {
+        for (int i = 0; i < kFewDepth; ++i) {  // 48 units: kDownWarps * kDownDepth
             const int v = warp + i * kFewWarps - Cs;
             if (v < 0 || v >= P.U * Ci) continue;
             const size_t row = (size_t)P.expert[v / Ci] * H + blockIdx.x * 16 + lane;
@@ -450,15 +452,15 @@ struct alignas(16) Unit {
 // touched ones as one long sum, its chunks (units) dealt out to the CTA's
 // warps: unit v to warp v mod 16, the shared expert's chunks first.
 template <int NT, bool kCoarse>
-__global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
+__global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ FewPicks P;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
     const int T = a.T;
-    constexpr int kRed = kFewWarps * 4 * NT * 16;
-    float* red = reinterpret_cast<float*>(smem + kFewWarps * kFewDepth * kStageBytes);  // [2][warp][4 NT][16]
-    const uint32_t ring = smem_addr(smem + warp * (kFewDepth * kStageBytes));
+    constexpr int kRed = kDownWarps * 4 * NT * 16;
+    float* red = reinterpret_cast<float*>(smem + kDownWarps * kDownDepth * kStageBytes);  // [2][warp][4 NT][16]
+    const uint32_t ring = smem_addr(smem + warp * (kDownDepth * kStageBytes));
     const int Cs = (a.Is + kChunkK - 1) / kChunkK, Ci = (a.I + kChunkK - 1) / kChunkK;
     const int tiles = a.H / 16;
     int units = Cs;  // units of a tile, as far as they are known
@@ -482,12 +484,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
         d.tokens = sh ? (1u << T) - 1 : P.tokens[u];
         return d;
     };
-    for (int v = tid; v < Cs; v += kFewThreads) list[v] = describe(v);
+    for (int v = tid; v < Cs; v += kDownThreads) list[v] = describe(v);
     __syncthreads();
 
     int iv = warp, it = blockIdx.x, ahead = 0;  // next copy: unit and tile; stages filled before the picks are known
     uint32_t dst = ring + stage_at(lane);
-    const uint32_t dst_end = dst + kFewDepth * kStageBytes;
+    const uint32_t dst_end = dst + kDownDepth * kStageBytes;
     auto issue = [&]() {
         if (it < tiles && iv < units) {
             const Unit& d = list[iv];
@@ -498,9 +500,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
             for (int i = 1; i < 4; ++i) ip[i] = ip[i - 1] + 4 * half;
             issue_chunk(dst, ip, 0, d.c * kChunkK + (lane & 7) * 32 < d.I);
             dst += kStageBytes;
-            if (dst == dst_end) dst -= kFewDepth * kStageBytes;
+            if (dst == dst_end) dst -= kDownDepth * kStageBytes;
             ++ahead;
-            iv += kFewWarps;
+            iv += kDownWarps;
             if (all && iv >= units) {
                 iv = warp;
                 it += gridDim.x;
@@ -508,112 +510,100 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
         }
         cp_async_commit();
     };
-    for (int i = 0; i < kFewDepth; ++i) issue();
+    for (int i = 0; i < kDownDepth; ++i) issue();
 
     pdl_wait();
     pdl_release();
-    for (int i = tid; i < (int)(sizeof(FewPicks) / 4); i += kFewThreads)
+    for (int i = tid; i < (int)(sizeof(FewPicks) / 4); i += kDownThreads)
         reinterpret_cast<int*>(&P)[i] = __ldcg(reinterpret_cast<const int*>(a.picks) + i);
     __syncthreads();
     units = Cs + P.U * Ci;
-    for (int v = Cs + tid; v < units; v += kFewThreads) list[v] = describe(v);
+    for (int v = Cs + tid; v < units; v += kDownThreads) list[v] = describe(v);
     __syncthreads();
     all = true;
     if (iv >= units && warp < units) {
         iv = warp;
         it += gridDim.x;
     }
-    for (int i = ahead; i < kFewDepth; ++i) issue();  // see few_gate_up_kernel
+    for (int i = ahead; i < kDownDepth; ++i) issue();  // see few_gate_up_kernel
 
     const int8_t* hq_shared = a.hq + (size_t)T * a.K * 2 * a.I;
     const float* hs_shared = a.hs + T * a.K * a.I / 32;
     int slot = 0, parity = 0;
-    // What a unit takes besides the staged weights, loaded one unit ahead.
-    struct Operands {
-        float sc[4];
-        uint4 x[4];
-        float4 hv[2];
-        unsigned tokens;
-    };
     // This lane's B row (token 4 n + g / 2, part g % 2) and the block scales of
     // its D columns (token 4 n + q).  A token that did not pick the expert
     // takes the first that did: its columns' sums are not used.
-    auto load_h = [&](const Unit& d, int n, Operands& o) {
-        const int any = __ffs(o.tokens) - 1;
+    auto load_h = [&](const Unit& d, unsigned tokens, int n, uint4 (&x)[4], float4 (&hv)[2]) {
+        const int any = __ffs(tokens) - 1;
         int sb = 4 * n + (g >> 1), sd = 4 * n + q;
-        if (!((o.tokens >> sb) & 1u)) sb = any;
-        if (!((o.tokens >> sd) & 1u)) sd = any;
+        if (!((tokens >> sb) & 1u)) sb = any;
+        if (!((tokens >> sd) & 1u)) sd = any;
         if (d.u >= 0) {
             sb = P.slot[d.u][sb];
             sd = P.slot[d.u][sd];
         }
         const uint4* xp = reinterpret_cast<const uint4*>((d.u < 0 ? hq_shared : a.hq) + (2 * sb + (g & 1)) * d.I + d.c * kChunkK) + q;
         const float4* hp = reinterpret_cast<const float4*>((d.u < 0 ? hs_shared : a.hs) + (sd * d.I + d.c * kChunkK) / 32);
-        o.x[0] = __ldcg(xp);
-        o.x[1] = __ldcg(xp + 4);
-        o.hv[0] = __ldcg(hp);
+        x[0] = __ldcg(xp);
+        x[1] = __ldcg(xp + 4);
+        hv[0] = __ldcg(hp);
         if (d.c * kChunkK + 128 < d.I) {
-            o.x[2] = __ldcg(xp + 8);
-            o.x[3] = __ldcg(xp + 12);
-            o.hv[1] = __ldcg(hp + 1);
+            x[2] = __ldcg(xp + 8);
+            x[3] = __ldcg(xp + 12);
+            hv[1] = __ldcg(hp + 1);
         } else {  // half a chunk: the rest of the stage is not its row's
-            o.x[2] = o.x[3] = make_uint4(0, 0, 0, 0);
-            o.hv[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            x[2] = x[3] = make_uint4(0, 0, 0, 0);
+            hv[1] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
-    auto first_n = [&](unsigned tokens) { return NT > 1 && !(tokens & 15u) ? 1 : 0; };
-    int nv = warp, ni = blockIdx.x;  // the next unit to load, and its tile
+    // The rows' scales come from HBM and are loaded a unit ahead; h comes from L2.
+    float nsc[4];
     const int esh = a.stype == kScaleF32 ? 2 : 1;
-    auto load = [&](Operands& o) {
-        if (nv >= units || ni >= tiles) return;
-        const Unit& d = list[nv];
-        o.tokens = d.tokens;
+    auto load_scales = [&](int v, int i) {
+        const Unit& d = list[v];
         ScaleRows sr;
-        sr.p0 = d.s + (((ni * 16 + g) * d.G) << esh);
+        sr.p0 = d.s + (((i * 16 + g) * d.G) << esh);
         sr.p8 = sr.p0 + ((8 * d.G) << esh);
-        load_chunk_scales<kCoarse>(o.sc, sr, d.c, a.gshift, d.G, a.stype, q);
-        load_h(d, first_n(o.tokens), o);
-        nv += kFewWarps;
-        if (nv >= units) {
-            nv = warp;
-            ni += gridDim.x;
-        }
+        load_chunk_scales<kCoarse>(nsc, sr, d.c, a.gshift, d.G, a.stype, q);
     };
-    float acc[NT][2];
-    auto multiply = [&](Operands& o, int v) {
-        scale_values(o.sc, a.stype);
-        cp_async_wait<kFewDepth - 1>();
-        __syncwarp();
-        const uint32_t st = ring + slot * kStageBytes;
-        slot = slot == kFewDepth - 1 ? 0 : slot + 1;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (NT > 1 && !((o.tokens >> (4 * n)) & 15u)) continue;
-            if (NT > 1 && n != first_n(o.tokens)) load_h(list[v], n, o);
-            float t[2];
-            down_mma<kCoarse>(st, o.x, o.hv, o.sc, a.gshift, lane, t);
-            if ((o.tokens >> (4 * n + q)) & 1u) {
-                acc[n][0] += t[0];
-                acc[n][1] += t[1];
-            }
-        }
-        __syncwarp();
-        issue();
-    };
-    Operands A, B;
-    load(A);
+    if (warp < units && (int)blockIdx.x < tiles) load_scales(warp, blockIdx.x);
     for (int i = blockIdx.x; i < tiles; i += gridDim.x, parity ^= 1) {
+        float acc[NT][2] = {};
+        for (int v = warp; v < units; v += kDownWarps) {
+            const Unit& d = list[v];
+            const unsigned tokens = d.tokens;
+            uint4 x[4];
+            float4 hv[2];
+            int n = NT > 1 && !(tokens & 15u) ? 1 : 0;
+            load_h(d, tokens, n, x, hv);
+            float sc[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = 0.f;
-        for (int v = warp; v < units; v += 2 * kFewWarps) {  // two at a time: no operand moves between registers
-            load(B);
-            multiply(A, v);
-            if (v + kFewWarps >= units) {
-                A = B;
-                break;
+            for (int u = 0; u < 4; ++u) sc[u] = nsc[u];
+            if (v + kDownWarps < units) load_scales(v + kDownWarps, i);
+            else if (i + (int)gridDim.x < tiles) load_scales(warp, i + gridDim.x);
+            scale_values(sc, a.stype);
+            cp_async_wait<kDownDepth - 1>();
+            __syncwarp();
+            const uint32_t st = ring + slot * kStageBytes;
+            slot = slot == kDownDepth - 1 ? 0 : slot + 1;
+#pragma unroll 1
+            for (;;) {
+                float t[2];
+                down_mma<kCoarse>(st, x, hv, sc, a.gshift, lane, t);
+                if ((tokens >> (4 * n + q)) & 1u) {
+                    if (NT == 1 || n == 0) {
+                        acc[0][0] += t[0];
+                        acc[0][1] += t[1];
+                    } else {
+                        acc[NT - 1][0] += t[0];
+                        acc[NT - 1][1] += t[1];
+                    }
+                }
+                if (NT == 1 || n == 1 || !(tokens >> 4)) break;
+                load_h(d, tokens, n = 1, x, hv);
             }
-            load(A);
-            multiply(B, v + kFewWarps);
+            __syncwarp();
+            issue();
         }
         float* part = red + parity * kRed;
 #pragma unroll
@@ -629,7 +619,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_down_kernel(FewArgs a) {
             float v = a.flags & kFlagResidual ? __bfloat162float(a.x[o]) : 0.f;
             float y = 0.f;
 #pragma unroll
-            for (int w = 0; w < kFewWarps; ++w) y += part[(w * 4 * NT + t) * 16 + r];
+            for (int w = 0; w < kDownWarps; ++w) y += part[(w * 4 * NT + t) * 16 + r];
             v += y;
             if (a.flags & kFlagOutF32) static_cast<float*>(a.out)[o] = v;
             else static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
@@ -707,8 +697,8 @@ cudaError_t few_launch(const FewArgs& a, cudaStream_t stream) {
     e = few_launch_cluster(up, grid, cluster, smem, stream, a, nullptr);
     const int out_tiles = a.H / 16;
     if (e == cudaSuccess)
-        e = launch_pdl(down, dim3(out_tiles < d.sms ? out_tiles : d.sms), dim3(kFewThreads),
-                       few_smem_base<NT>() + sizeof(Unit) * ((a.Is + kChunkK - 1) / kChunkK +
+        e = launch_pdl(down, dim3(out_tiles < d.sms ? out_tiles : d.sms), dim3(kDownThreads),
+                       (size_t)kDownWarps * kDownDepth * kStageBytes + 2 * (size_t)kDownWarps * 4 * NT * 16 * 4 + sizeof(Unit) * ((a.Is + kChunkK - 1) / kChunkK +
                                                             (size_t)touched * ((a.I + kChunkK - 1) / kChunkK)),
                        stream, a);
     return e;
