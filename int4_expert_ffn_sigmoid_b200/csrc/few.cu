@@ -168,6 +168,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     };
     open_tile();
     for (int i = 0; i < kFewDepth; ++i) issue();
+    float nxt[4];  // the next chunk's scales, on their way while this one is multiplied
+    ScaleRows sr;
+    auto open_scales = [&](const Tile& t) {
+        sr.open(t.s, t.row + g, t.row + t.I + g, a.G13, a.stype);
+        if (per > 0) load_chunk_scales<kCoarse>(nxt, sr, j, a.gshift, a.G13, a.stype, q);
+    };
+    if ((int)blockIdx.x < shared_tiles) open_scales(tile(blockIdx.x));
 
     // Before the wait: the router's constants, and the tables' initial state.
     const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -177,6 +184,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     if (tid < kMaxE / 32) s_mask[tid] = 0;
     if (tid < kFewMaxU) P.tokens[tid] = 0;
     if (tid < kFewMaxU * kFewTok) P.slot[tid / kFewTok][tid % kFewTok] = -1;
+    static_assert(kFewCluster <= 8, "a lane of eight per CTA");
     static_assert(kFewThreads >= kFewMaxU * kFewTok, "one slot a thread");
     // The dot product of this warp's experts e_lo + warp, + 16, ...: eight
     // 128-column blocks of weights at a time, the next ones on their way.
@@ -216,12 +224,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
             s_logit[i / a.E][i % a.E] = v;
         }
     } else {
-        float acc[kFewTok] = {};
+        float acc[4 * NT] = {};
         for (int b = 0; e < e_hi;) {
             float4 w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = wn[i];
-            const int e_now = e, b_now = b;
+            const int e_now = e, nb = min(8, H / 128 - b);
+            const uint2* xb = reinterpret_cast<const uint2*>(x + b * 128) + lane;
             b += 8;
             const bool last = b >= H / 128;
             if (last) {
@@ -229,50 +238,62 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
                 e += kFewWarps;
             }
             if (e < e_hi) load_w(e, b);
-            const int nb = min(8, H / 128 - b_now);
-#pragma unroll
-            for (int t = 0; t < kFewTok; ++t) {
-                if (t >= T) break;
-                const uint2* xt = reinterpret_cast<const uint2*>(x + (size_t)t * H + b_now * 128) + lane;
+            auto dot = [&](float& o, const uint2* xt) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if (i >= nb) break;
                     const uint2 xv = xt[i * 32];
-                    acc[t] = fmaf(bf16lo(xv.x), w[i].x, acc[t]);
-                    acc[t] = fmaf(bf16hi(xv.x), w[i].y, acc[t]);
-                    acc[t] = fmaf(bf16lo(xv.y), w[i].z, acc[t]);
-                    acc[t] = fmaf(bf16hi(xv.y), w[i].w, acc[t]);
+                    o = fmaf(bf16lo(xv.x), w[i].x, o);
+                    o = fmaf(bf16hi(xv.x), w[i].y, o);
+                    o = fmaf(bf16lo(xv.y), w[i].z, o);
+                    o = fmaf(bf16hi(xv.y), w[i].w, o);
                 }
+            };
+            // One token, or all 4 NT of the tile (past the last, it again): four
+            // independent chains instead of one after another.
+            if (T == 1) {
+                dot(acc[0], xb);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4 * NT; ++t) dot(acc[t], xb + (size_t)min(t, T - 1) * (H / 4));
             }
             if (!last) continue;
+            // The 32 lanes' sums, lane pairs 16, 8, 4, 2, 1 apart in turn: for
+            // four tokens at once the first two exchanges halve what a lane
+            // holds, and lanes 8 t .. 8 t + 7 end with token t.
 #pragma unroll
-            for (int t = 0; t < kFewTok; ++t) {
-                if (t >= T) break;
-                float v = acc[t];
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane < size) *cluster.map_shared_rank(&s_logit[t][e_now], lane) = v;
-                acc[t] = 0.f;
+            for (int n = 0; n < NT; ++n) {
+                float* v = acc + 4 * n;
+                const bool up = lane & 16, odd = lane & 8;
+                const float a0 = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+                const float a1 = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+                float s = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 8);
+                s += __shfl_xor_sync(0xffffffffu, s, 4);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                const int t = 4 * n + (lane >> 3);
+                if (t < T && (lane & 7) < size) *cluster.map_shared_rank(&s_logit[t][e_now], lane & 7) = s;
+                v[0] = v[1] = v[2] = v[3] = 0.f;
             }
         }
     }
+    if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
     // int8 activations, while the cluster's other logits arrive
     if (a.lslices == 0)
         quantize_tokens<kCoarse>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
-    if (size > 1) cluster.sync();
-    else __syncthreads();
-
-    // Scores (two warps a token, rolled: this code runs once a launch and is
-    // fetched cold), the picks (a warp a token), the tables.
-    if ((warp & 7) < T) {
-        float* s = s_logit[warp & 7];
-#pragma unroll 1
-        for (int i = (warp >> 3) * 32 + lane; i < a.E; i += 64) s[i] = 1.0f / (1.0f + expf(-s[i]));
-    }
+    if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
+
+    // Scores (a short loop: this code runs once a launch and is fetched cold)
+    // and picks, a warp a token; then the tables.
     int my_e = -1;
     float my_w = 0.f;
     if (warp < T) {
+        float* s = s_logit[warp];
+#pragma unroll 2
+        for (int i = lane; i < a.E; i += 32) s[i] = 1.0f / (1.0f + expf(-s[i]));
+        __syncwarp();
         few_select(a, s_logit[warp], s_bias, lane, my_e, my_w);
         if (lane < a.K) {
             if (my_e >= 0) atomicOr(&s_mask[my_e >> 5], 1u << (my_e & 31));
@@ -310,23 +331,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         // n-th stage is then never among the last kFewDepth - 1 when it is read.
         for (int i = ahead; i < kFewDepth; ++i) issue();
     }
-    // With its last copy issued, the CTA brings what the down kernel's CTA of
-    // the same index reads first (a ring's worth of routed units) into L2.
-    bool last_issued = false;
-    auto prefetch_down = [&]() {
-        if (last_issued || it < known) return;
-        last_issued = true;
-        const int Cs = (a.Is + kChunkK - 1) / kChunkK, Ci = (a.I + kChunkK - 1) / kChunkK;
-        if ((int)blockIdx.x >= H / 16 || lane >= 16) return;
-        for (int i = 0; i < kFewDepth; ++i) {  // 48 units: kDownWarps * kDownDepth
-            const int v = warp + i * kFewWarps - Cs;
-            if (v < 0 || v >= P.U * Ci) continue;
-            const size_t row = (size_t)P.expert[v / Ci] * H + blockIdx.x * 16 + lane;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.w2 + row * (a.I / 2) + v % Ci * (kChunkK / 2)));
-        }
-    };
-    prefetch_down();
-
     uint32_t xrow[NT];
     const float* xsc[NT];
 #pragma unroll
@@ -336,14 +340,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         xsc[n] = xs + min(4 * n + q, T - 1);
     }
     int slot = 0, parity = 0;
-    float nxt[4];  // the next chunk's scales, on their way while this one is multiplied
-    ScaleRows sr;
-    auto open_scales = [&](const Tile& t) {
-        sr.open(t.s, t.row + g, t.row + t.I + g, a.G13, a.stype);
-        if (per > 0) load_chunk_scales<kCoarse>(nxt, sr, j, a.gshift, a.G13, a.stype, q);
-    };
     Tile t;
-    if (blockIdx.x < known) open_scales(t = tile(blockIdx.x));
+    if ((int)blockIdx.x >= shared_tiles && (int)blockIdx.x < known) open_scales(tile(blockIdx.x));
+    if ((int)blockIdx.x < known) t = tile(blockIdx.x);
     for (int i = blockIdx.x; i < known; i += gridDim.x, parity ^= 1) {
         Tile after = t;
         if (per == 0 && i + (int)gridDim.x < known) after = tile(i + gridDim.x);
@@ -372,7 +371,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
             }
             __syncwarp();
             issue();
-            prefetch_down();
         }
         float* part = red + parity * kRed;
 #pragma unroll
@@ -511,6 +509,17 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
         cp_async_commit();
     };
     for (int i = 0; i < kDownDepth; ++i) issue();
+    // The rows' scales come from HBM and are loaded a unit ahead; h comes from L2.
+    float nsc[4];
+    const int esh = a.stype == kScaleF32 ? 2 : 1;
+    auto load_scales = [&](int v, int i) {
+        const Unit& d = list[v];
+        ScaleRows sr;
+        sr.p0 = d.s + (((i * 16 + g) * d.G) << esh);
+        sr.p8 = sr.p0 + ((8 * d.G) << esh);
+        load_chunk_scales<kCoarse>(nsc, sr, d.c, a.gshift, d.G, a.stype, q);
+    };
+    if (warp < Cs && (int)blockIdx.x < tiles) load_scales(warp, blockIdx.x);
 
     pdl_wait();
     pdl_release();
@@ -556,17 +565,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
             hv[1] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
-    // The rows' scales come from HBM and are loaded a unit ahead; h comes from L2.
-    float nsc[4];
-    const int esh = a.stype == kScaleF32 ? 2 : 1;
-    auto load_scales = [&](int v, int i) {
-        const Unit& d = list[v];
-        ScaleRows sr;
-        sr.p0 = d.s + (((i * 16 + g) * d.G) << esh);
-        sr.p8 = sr.p0 + ((8 * d.G) << esh);
-        load_chunk_scales<kCoarse>(nsc, sr, d.c, a.gshift, d.G, a.stype, q);
-    };
-    if (warp < units && (int)blockIdx.x < tiles) load_scales(warp, blockIdx.x);
+    if (warp >= Cs && warp < units && (int)blockIdx.x < tiles) load_scales(warp, blockIdx.x);
     for (int i = blockIdx.x; i < tiles; i += gridDim.x, parity ^= 1) {
         float acc[NT][2] = {};
         for (int v = warp; v < units; v += kDownWarps) {

@@ -18,7 +18,7 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kXMax = 96 * 1024;
 
 struct StreamPlan {
-    int wk_log, wr_log;  // warps along the columns, teams: 1 << each
+    int wk_log, wr;      // warps along the columns: 1 << wk_log; teams
     int chunks, tiles;   // 256-column chunks of a row; CTA tiles of 16 rows a team
 };
 
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
     // this warp's chunks, tile after tile
     const int per = j < p.chunks ? ((p.chunks - j - 1) >> p.wk_log) + 1 : 0;
     const int tiles = p.tiles > (int)blockIdx.x ? (p.tiles - blockIdx.x - 1) / gridDim.x + 1 : 0;
-    const int rows_cta = 16 << p.wr_log, last = a.N - 1, half = a.K / 2;
+    const int rows_cta = 16 * p.wr, last = a.N - 1, half = a.K / 2;
     int left = per * tiles;  // copies to issue
     int ir = blockIdx.x * rows_cta + team * 16, ic = j;  // row and chunk of the next copy
     uint32_t dst = ring + stage_at(lane);
@@ -91,7 +91,20 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
         xsc[n] = xs + min(4 * n + q, a.T - 1);
     }
     int slot = 0;
+    // Output o of a tile: row o mod 16 of team (o / 16) mod wr, token o / (16 wr).
+    const int outs = a.T * rows_cta;
+    auto place = [&](int o, int& t, int& tm, int& n) {
+        t = o / rows_cta;
+        tm = (o - t * rows_cta) >> 4;
+        n = row - team * 16 + o - t * rows_cta;
+        return n < a.N;
+    };
     for (int i = 0; i < tiles; ++i, row += rows_cta * gridDim.x) {
+        float plus = 0.f;  // what the thread's first output is added to: on its way during the products
+        if (a.add && tid < outs) {
+            int t, tm, n;
+            if (place(tid, t, tm, n)) plus = __bfloat162float(a.add[t * a.lda + n]);
+        }
         float acc[NT][2] = {};
         for (int c = j; c < p.chunks; c += wk) {
             float sc[4];
@@ -129,13 +142,12 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
             o[g + 8] = acc[n][1];
         }
         __syncthreads();
-        for (int o = tid; o < (a.T * 16 << p.wr_log); o += 32 * NW) {
-            const int r = o & 15, tm = (o >> 4) & ((1 << p.wr_log) - 1), t = o >> (4 + p.wr_log);
-            const int n = row - team * 16 + tm * 16 + r;
-            if (n >= a.N) continue;
+        for (int o = tid; o < outs; o += 32 * NW) {
+            int t, tm, n;
+            if (!place(o, t, tm, n)) continue;
             float v = 0.f;
-            for (int u = 0; u < wk; ++u) v += part[(((tm << p.wk_log) + u) * 4 * NT + t) * 16 + r];
-            if (a.add) v += __bfloat162float(a.add[t * a.lda + n]);
+            for (int u = 0; u < wk; ++u) v += part[(((tm << p.wk_log) + u) * 4 * NT + t) * 16 + (o & 15)];
+            if (a.add) v += o == tid ? plus : __bfloat162float(a.add[t * a.lda + n]);
             if (a.out_f32) static_cast<float*>(a.out)[t * a.ldo + n] = v;
             else static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + n] = __float2bfloat16_rn(v);
         }
@@ -170,19 +182,14 @@ cudaError_t launch_stream(const LinearArgs& a, StreamPlan p, cudaStream_t stream
         set[dev] = 1;
     }
     const int per_sm = NW == 8 ? (3 * smem <= kSmemMax - 3 * 1024 ? 3 : 2 * smem <= kSmemMax - 2 * 1024 ? 2 : 1) : 1;
-    p.tiles = (a.N + (16 << p.wr_log) - 1) >> (4 + p.wr_log);
+    p.tiles = (a.N + 16 * p.wr - 1) / (16 * p.wr);
     const int grid = p.tiles < per_sm * sms() ? p.tiles : per_sm * sms();
     return launch_pdl(k, dim3(grid), dim3(32 * NW), smem, stream, a, p);
 }
 
-template <int NW>
+template <int NW, int NT>
 cudaError_t launch_stream(const LinearArgs& a, const StreamPlan& p, cudaStream_t stream) {
-    const bool coarse = a.gshift >= 7;
-    if constexpr (NW == 16) {
-        if (a.T > 8) return coarse ? launch_stream<NW, 4, true>(a, p, stream) : launch_stream<NW, 4, false>(a, p, stream);
-        if (a.T > 4) return coarse ? launch_stream<NW, 2, true>(a, p, stream) : launch_stream<NW, 2, false>(a, p, stream);
-    }
-    return coarse ? launch_stream<NW, 1, true>(a, p, stream) : launch_stream<NW, 1, false>(a, p, stream);
+    return a.gshift >= 7 ? launch_stream<NW, NT, true>(a, p, stream) : launch_stream<NW, NT, false>(a, p, stream);
 }
 
 int stream_tokens(const LinearArgs& a) {
@@ -198,11 +205,18 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
     if (a.T > stream_tokens(a)) return launch_linear_gemm(a, stream);
     StreamPlan p = {};
     p.chunks = (a.K + kChunkK - 1) / kChunkK;
-    const int nw_log = a.T <= 2 ? 3 : 4;
-    for (p.wk_log = 0; p.wk_log < nw_log && (1 << p.wk_log) < p.chunks; ++p.wk_log) {}
-    if (p.wk_log > 3 && p.chunks < 32) p.wk_log = 3;
-    p.wr_log = nw_log - p.wk_log;
-    return nw_log == 3 ? launch_stream<8>(a, p, stream) : launch_stream<16>(a, p, stream);
+    for (p.wk_log = 0; p.wk_log < 3 && (1 << p.wk_log) < p.chunks; ++p.wk_log) {}
+    auto teams = [&](int warps) {
+        p.wr = warps >> p.wk_log;
+        return p;
+    };
+    if (a.T > 8) return launch_stream<16, 4>(a, teams(16), stream);
+    if (a.T > 4) return launch_stream<16, 2>(a, teams(16), stream);
+    // 24 warps share the activations' rounding, where that leaves a tile for
+    // most SMs; else eight a CTA and three CTAs a SM (measured, one token:
+    // LATER).
+    if (a.N >= 16 * (24 >> p.wk_log) * 96) return launch_stream<24, 1>(a, teams(24), stream);
+    return launch_stream<8, 1>(a, teams(8), stream);
 }
 
 }  // namespace moe
