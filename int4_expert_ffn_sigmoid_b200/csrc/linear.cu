@@ -18,7 +18,7 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kXMax = 96 * 1024;
 
 struct StreamPlan {
-    int wk_log, wr;      // warps along the columns: 1 << wk_log; teams
+    int wk_log, wr_log;  // warps along the columns, teams: 1 << each
     int chunks, tiles;   // 256-column chunks of a row; CTA tiles of 16 rows a team
 };
 
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
     // this warp's chunks, tile after tile
     const int per = j < p.chunks ? ((p.chunks - j - 1) >> p.wk_log) + 1 : 0;
     const int tiles = p.tiles > (int)blockIdx.x ? (p.tiles - blockIdx.x - 1) / gridDim.x + 1 : 0;
-    const int rows_cta = 16 * p.wr, last = a.N - 1, half = a.K / 2;
+    const int rows_cta = 16 << p.wr_log, last = a.N - 1, half = a.K / 2;
     int left = per * tiles;  // copies to issue
     int ir = blockIdx.x * rows_cta + team * 16, ic = j;  // row and chunk of the next copy
     uint32_t dst = ring + stage_at(lane);
@@ -91,19 +91,18 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
         xsc[n] = xs + min(4 * n + q, a.T - 1);
     }
     int slot = 0;
-    // Output o of a tile: row o mod 16 of team (o / 16) mod wr, token o / (16 wr).
+    // Output o of a tile: its row o mod rows_cta, token o / rows_cta.
     const int outs = a.T * rows_cta;
-    auto place = [&](int o, int& t, int& tm, int& n) {
-        t = o / rows_cta;
-        tm = (o - t * rows_cta) >> 4;
-        n = row - team * 16 + o - t * rows_cta;
+    auto place = [&](int o, int& t, int& n) {
+        t = o >> (4 + p.wr_log);
+        n = row - team * 16 + (o & (rows_cta - 1));
         return n < a.N;
     };
     for (int i = 0; i < tiles; ++i, row += rows_cta * gridDim.x) {
         float plus = 0.f;  // what the thread's first output is added to: on its way during the products
         if (a.add && tid < outs) {
-            int t, tm, n;
-            if (place(tid, t, tm, n)) plus = __bfloat162float(a.add[t * a.lda + n]);
+            int t, n;
+            if (place(tid, t, n)) plus = __bfloat162float(a.add[t * a.lda + n]);
         }
         float acc[NT][2] = {};
         for (int c = j; c < p.chunks; c += wk) {
@@ -143,8 +142,9 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
         }
         __syncthreads();
         for (int o = tid; o < outs; o += 32 * NW) {
-            int t, tm, n;
-            if (!place(o, t, tm, n)) continue;
+            int t, n;
+            if (!place(o, t, n)) continue;
+            const int tm = (o & (rows_cta - 1)) >> 4;
             float v = 0.f;
             for (int u = 0; u < wk; ++u) v += part[(((tm << p.wk_log) + u) * 4 * NT + t) * 16 + (o & 15)];
             if (a.add) v += o == tid ? plus : __bfloat162float(a.add[t * a.lda + n]);
@@ -182,7 +182,7 @@ cudaError_t launch_stream(const LinearArgs& a, StreamPlan p, cudaStream_t stream
         set[dev] = 1;
     }
     const int per_sm = NW == 8 ? (3 * smem <= kSmemMax - 3 * 1024 ? 3 : 2 * smem <= kSmemMax - 2 * 1024 ? 2 : 1) : 1;
-    p.tiles = (a.N + 16 * p.wr - 1) / (16 * p.wr);
+    p.tiles = (a.N + (16 << p.wr_log) - 1) >> (4 + p.wr_log);
     const int grid = p.tiles < per_sm * sms() ? p.tiles : per_sm * sms();
     return launch_pdl(k, dim3(grid), dim3(32 * NW), smem, stream, a, p);
 }
@@ -205,18 +205,18 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
     if (a.T > stream_tokens(a)) return launch_linear_gemm(a, stream);
     StreamPlan p = {};
     p.chunks = (a.K + kChunkK - 1) / kChunkK;
-    for (p.wk_log = 0; p.wk_log < 3 && (1 << p.wk_log) < p.chunks; ++p.wk_log) {}
+    while (p.wk_log < 3 && (1 << p.wk_log) < p.chunks) ++p.wk_log;
     auto teams = [&](int warps) {
-        p.wr = warps >> p.wk_log;
+        p.wr_log = (warps == 8 ? 3 : 4) - p.wk_log;
         return p;
     };
-    if (a.T > 8) return launch_stream<16, 4>(a, teams(16), stream);
-    if (a.T > 4) return launch_stream<16, 2>(a, teams(16), stream);
-    // 24 warps share the activations' rounding, where that leaves a tile for
-    // most SMs; else eight a CTA and three CTAs a SM (measured, one token:
-    // LATER).
-    if (a.N >= 16 * (24 >> p.wk_log) * 96) return launch_stream<24, 1>(a, teams(24), stream);
-    return launch_stream<8, 1>(a, teams(8), stream);
+    // Up to two tokens, eight warps a CTA and three CTAs an SM: the finest
+    // tiles (one token x 1024 x 1024: 2.0 us against 2.2 with 16 warps).  More
+    // tokens: 16 warps share their rounding to int8 (four tokens x 12288 x 6144:
+    // 13.8 us; 24 warps, which leave 80 registers a thread, 14.3).
+    if (a.T <= 2) return launch_stream<8, 1>(a, teams(8), stream);
+    if (a.T <= 4) return launch_stream<16, 1>(a, teams(16), stream);
+    return a.T <= 8 ? launch_stream<16, 2>(a, teams(16), stream) : launch_stream<16, 4>(a, teams(16), stream);
 }
 
 }  // namespace moe
