@@ -521,7 +521,8 @@ class Int4Linear:
         odt = torch.float32 if flags & MOE_OUT_F32 else torch.bfloat16
         ldx, ldo, lda, ap = _rows_of("x", x, torch.bfloat16, (T, self.K), device), 0, 0, None
         if out is None:
-            out = x.new_empty((T, self.N)) if not flags else x.new_empty((T, self.N), dtype=odt)
+            with _NO_GUARD if stream is None else torch.cuda.stream(stream):
+                out = x.new_empty((T, self.N)) if not flags else x.new_empty((T, self.N), dtype=odt)
         else:
             ldo = _rows_of("out", out, odt, (T, self.N), device)
         if add is not None:
@@ -627,7 +628,8 @@ class MoEFewLayer:
         f = flags | (MOE_ADD_RESIDUAL if residual else 0)
         odt = torch.float32 if f & MOE_OUT_F32 else torch.bfloat16
         if out is None:
-            out = x.new_empty((T, shape.H), dtype=odt, device=self.device)
+            with _NO_GUARD if stream is None else torch.cuda.stream(stream):
+                out = x.new_empty((T, shape.H), dtype=odt)
         ws = self.workspace if workspace is None else workspace
         self._check("x", x, torch.bfloat16, (T, shape.H))
         self._check("out", out, odt, (T, shape.H))
@@ -656,7 +658,6 @@ def few_forward(x: torch.Tensor, layer: dict, shape, group: int = 0, out: Option
                 flags: int = 0, topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
                 stream: Optional[torch.cuda.Stream] = None, topp: float = 0.0) -> torch.Tensor:
     """One call of ``MoEFewLayer``, with a workspace of its own."""
-    m = MoEFewLayer(layer, shape, group, max_tokens=max(1, x.shape[0]), topp=topp)
-    if stream is not None:
-        m.workspace.record_stream(stream)  # freed when this call returns: not before the stream is through with it
+    with torch.cuda.stream(stream):  # the workspace belongs to the stream that uses it
+        m = MoEFewLayer(layer, shape, group, max_tokens=max(1, x.shape[0]), topp=topp)
     return m(x, out=out, flags=flags, topk_idx=topk_idx, topk_w=topk_w, stream=stream)

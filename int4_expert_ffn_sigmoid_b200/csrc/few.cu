@@ -199,16 +199,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     // Behind the logits kernel x is final: that kernel let this one start only
     // after its own wait for whatever wrote x.
     if (a.lslices > 0)
-        quantize_tokens<kCoarse>(a.x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
+        quantize_tokens<kCoarse, true>(a.x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
     pdl_wait();
     pdl_release();
 
     // x in shared memory where it fits the room of the partial sums
     const __nv_bfloat16* x = a.x;
-    if (a.lslices == 0 && (size_t)T * H * 2 <= 2 * kRed * 4) {
+    const bool staged = a.lslices == 0 && (size_t)T * H * 2 <= 2 * kRed * 4;
+    if (staged) {
         __nv_bfloat16* xr = reinterpret_cast<__nv_bfloat16*>(red);
         for (int i = tid; i < T * H / 8; i += kFewThreads)
-            reinterpret_cast<uint4*>(xr)[i] = __ldg(reinterpret_cast<const uint4*>(a.x) + i);
+            reinterpret_cast<uint4*>(xr)[i] = __ldcg(reinterpret_cast<const uint4*>(a.x) + i);
         x = xr;
         __syncthreads();
     }
@@ -280,8 +281,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
     // int8 activations, while the cluster's other logits arrive
-    if (a.lslices == 0)
-        quantize_tokens<kCoarse>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
+    if (a.lslices == 0) {
+        if (staged) quantize_tokens<kCoarse, false>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
+        else quantize_tokens<kCoarse, true>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
+    }
     if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
 
@@ -439,12 +442,13 @@ __device__ __forceinline__ void down_mma(uint32_t stage, const uint4 (&x)[4], co
     }
 }
 
-struct alignas(16) Unit {
+struct Unit {  // 24 bytes: up to 2080 of them beside the rings (I = Is = 8192, 64 experts)
     const uint8_t* w;
     const char* s;
-    int u, c, I, G;
-    unsigned tokens;
+    int16_t u, I, G;
+    uint8_t c, tokens;
 };
+static_assert(sizeof(Unit) == 24, "packed");
 
 // Down projection of whole output tiles: 16 rows, the shared expert and all
 // touched ones as one long sum, its chunks (units) dealt out to the CTA's
@@ -473,13 +477,13 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
         const bool sh = v < Cs;
         const int u = sh ? -1 : (v - Cs) / Ci, c = sh ? v : v - Cs - u * Ci;
         const size_t row = sh ? 0 : (size_t)P.expert[u] * a.H;
-        d.I = sh ? a.Is : a.I;
-        d.G = sh ? a.Gs2 : a.G2;
+        d.I = (int16_t)(sh ? a.Is : a.I);
+        d.G = (int16_t)(sh ? a.Gs2 : a.G2);
         d.w = (sh ? a.sh_w2 : a.w2) + row * (d.I / 2) + c * (kChunkK / 2);
         d.s = static_cast<const char*>(sh ? a.sh_s2 : a.s2) + ((row * d.G) << (a.stype == kScaleF32 ? 2 : 1));
-        d.u = u;
-        d.c = c;
-        d.tokens = sh ? (1u << T) - 1 : P.tokens[u];
+        d.u = (int16_t)u;
+        d.c = (uint8_t)c;
+        d.tokens = (uint8_t)(sh ? (1u << T) - 1 : P.tokens[u]);
         return d;
     };
     for (int v = tid; v < Cs; v += kDownThreads) list[v] = describe(v);
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
     // its D columns (token 4 n + q).  A token that did not pick the expert
     // takes the first that did: its columns' sums are not used.
     auto load_h = [&](const Unit& d, unsigned tokens, int n, uint4 (&x)[4], float4 (&hv)[2]) {
-        const int any = __ffs(tokens) - 1;
+        const int any = __ffs((int)tokens) - 1;
         int sb = 4 * n + (g >> 1), sd = 4 * n + q;
         if (!((tokens >> sb) & 1u)) sb = any;
         if (!((tokens >> sd) & 1u)) sd = any;

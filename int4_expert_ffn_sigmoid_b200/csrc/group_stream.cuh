@@ -105,8 +105,9 @@ __device__ __forceinline__ void quantize_chunk(uint4 v, int8_t* q0, int8_t* q1, 
 
 // All chunks of nt tokens (x: the first token's row, ldx elements apart, K
 // columns) over the CTA's nw warps, four loads in flight a warp; token t's
-// scale of chunk c goes to xs[c * xs_tok + t].
-template <bool kCoarse>
+// scale of chunk c goes to xs[c * xs_tok + t].  kGlobal: x is in global
+// memory (read from L2: what the previous kernel wrote), else in shared memory.
+template <bool kCoarse, bool kGlobal>
 __device__ __forceinline__ void quantize_tokens(const __nv_bfloat16* x, long long ldx, int K, int chunks, int nt,
                                                 int8_t* xq, int xs_bytes, float* xs, int xs_tok, int warp, int nw,
                                                 int lane) {
@@ -120,7 +121,8 @@ __device__ __forceinline__ void quantize_tokens(const __nv_bfloat16* x, long lon
             t[u] = i / chunks;
             c[u] = i - t[u] * chunks;
             const int k = c[u] * kChunkK + 8 * lane;
-            v[u] = t[u] < nt && k < K ? *reinterpret_cast<const uint4*>(x + t[u] * ldx + k) : make_uint4(0, 0, 0, 0);
+            const uint4* p = reinterpret_cast<const uint4*>(x + t[u] * ldx + k);
+            v[u] = t[u] >= nt || k >= K ? make_uint4(0, 0, 0, 0) : kGlobal ? __ldcg(p) : *p;
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {

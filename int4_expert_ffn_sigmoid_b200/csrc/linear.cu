@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
     pdl_wait();
     pdl_release();
 
-    quantize_tokens<kCoarse>(a.x, a.ldx, a.K, p.chunks, a.T, xq, xs_bytes, xs, 4 * NT, warp, NW, lane);
+    quantize_tokens<kCoarse, true>(a.x, a.ldx, a.K, p.chunks, a.T, xq, xs_bytes, xs, 4 * NT, warp, NW, lane);
     __syncthreads();
 
     uint32_t xrow[NT];  // a column past the last token repeats it: its sums are not stored

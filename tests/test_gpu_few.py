@@ -248,3 +248,37 @@ def test_binding_refusals(moe, cuda_device):
         moe.MoEFewLayer(L, shape, 64)
     with pytest.raises(moe.MoeError):
         moe.MoEFewLayer(L, shape_of(256, 4, 2, 130, 128), 32)
+
+
+@pytest.mark.parametrize("dims,T,group", [
+    ((128, 64, 8, 8192, 8192, 1.0), 8, 32),    # the longest list of down units
+    ((6144, 16, 8, 128, 128, 2.5), 8, 64),     # the most activations beside the rings
+    ((7168, 8, 2, 128, 256, 1.0), 7, 128),     # a token more than fits: two passes
+    ((6912, 8, 2, 128, 256, 1.0), 7, 128),
+    ((16384, 8, 1, 128, 0, 1.0), 3, 32768),
+])
+def test_largest_shared_memory(moe, cuda_device, dims, T, group):
+    shape = shape_of(*dims)
+    L = make_layer(shape, group, "bf16", seed=1, device=cuda_device)
+    assert moe.few_pass_tokens(shape, group) == (6 if shape.H == 7168 else T)
+    check(moe, tokens(T, shape, L, 12, cuda_device), L, shape, group)
+
+
+def test_split_router_passes(moe, cuda_device):
+    """Router weights past the cluster's share: the logits kernel in front, in two passes, replayed."""
+    shape = shape_of(2048, 256, 8, 128, 128)
+    L = make_layer(shape, 128, "f32", device=cuda_device)
+    assert moe.few_kernel_launches(shape, 8, 128) == 3 and moe.few_kernel_launches(shape, 13, 128) == 6
+    assert moe.few_kernel_launches(shape_of(512, 256, 8, 128, 128), 8, 128) == 2
+    x = tokens(13, shape, L, 31, cuda_device)
+    out = check(moe, x, L, shape, 128, residual=True, max_tokens=13)
+    m = moe.MoEFewLayer(L, shape, 128, max_tokens=13)
+    got = torch.empty_like(out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m(x, out=got, residual=True)
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)

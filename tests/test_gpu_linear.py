@@ -200,3 +200,55 @@ def test_binding_refusals(moe, cuda_device):
         moe.Int4Linear(w, scales(gen(0, cuda_device), (64,), 128, 48), 48)  # not a power of two
     with pytest.raises(moe.MoeError):
         lin(x, out=x[:, :64])  # overlaps x
+
+
+FIRST_CALL = """
+import torch
+import int4_expert_ffn_sigmoid_b200 as moe
+from tests._group_int4 import codes, gen, make_layer, scales, shape_of
+dev = torch.device("cuda:0")
+g = gen(1, dev)
+cases = [(1, 320, 1024), (6, 320, 1024), (40, 320, 1024), (300, 320, 1024)]
+lins = [(moe.Int4Linear(codes(g, N, K // 2), scales(g, (N,), K, 32), 32), torch.randn((T, K), device=dev).bfloat16())
+        for T, N, K in cases]
+shape = shape_of(1024, 8, 2, 128, 128)
+few = moe.MoEFewLayer(make_layer(shape, 32, device=dev), shape, 32)
+v = torch.randn((2, 1024), device=dev).bfloat16()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = [l(x) for l, x in lins] + [few(v)]
+graph.replay()
+torch.cuda.synchronize()
+for o, w in zip(outs, [l(x) for l, x in lins] + [few(v)]):
+    assert torch.equal(o, w)
+print("same")
+"""
+
+
+def test_first_call_inside_a_capture(cuda_device):
+    """A process whose first calls are captured: nothing is set up outside."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+def test_side_stream_tensors(moe, cuda_device):
+    """Inputs made and outputs used on a stream of their own."""
+    st = torch.cuda.Stream()
+    x, w, s, a = make(5, 640, 512, 64, "bf16", 3, True, cuda_device)
+    lin = moe.Int4Linear(w, s, 64)
+    want = lin(x, add=a)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(50):
+            y = x.clone()
+            got = lin(y, add=a)
+            del y
+    st.synchronize()
+    assert torch.equal(got, want)
+    got = lin(x, add=a, stream=st)
+    st.synchronize()
+    assert torch.equal(got, want)
