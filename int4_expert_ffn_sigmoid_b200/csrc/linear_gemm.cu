@@ -19,8 +19,8 @@
 // its parts in shared memory (rank c % size takes tokens 8 c .. 8 c + 7) and
 // stores them; in the same order every time.
 //
-// Roles (864 threads, one CTA per SM): warps 0-23 convert (three groups of
-// eight take the stages in turn) and then read the accumulators out; warps 24
+// Roles (864 threads, one CTA per SM): warps 0-23 convert (in groups
+// that take the stages in turn) and then read the accumulators out; warps 24
 // and 25 issue the TMA loads of the codes and of x, warp 26 the MMAs.  Every wait is bounded; a CTA whose wait
 // gave up (never, in a correct run) stores NaN.
 #include <cooperative_groups.h>
@@ -33,10 +33,10 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 128, kStageK = 128;
-constexpr int kGroups = 3, kConvWarps = 8 * kGroups, kThreads = 32 * (kConvWarps + 3);
+constexpr int kConvWarps = 24, kThreads = 32 * (kConvWarps + 3);
 constexpr int kWarpW = kConvWarps, kWarpX = kConvWarps + 1, kWarpMma = kConvWarps + 2;
 constexpr int kColGroups = kConvWarps / 4;  // warps of a lane quarter, for reading the accumulators
-constexpr int kACols = 64, kACol0 = 256;  // tensor memory: D in columns 0-255, then the A stages
+constexpr int kACols = 64;  // tensor memory columns of an A stage
 constexpr int kTmemCols = 512;
 constexpr int kWBytes = kRows * kStageK / 2;
 constexpr long long kWait = kBulkWaitCycles;
@@ -46,12 +46,24 @@ struct Geo {
     // Stages of x and of A go together: the one commit after a stage's MMAs
     // frees both.  The codes have a deeper ring of their own.
     static constexpr int kXBytes = kN * kStageK * 2;
-    static constexpr int kStages = kN == 256 ? 3 : 4;
-    static constexpr int kWStages = kN == 256 ? 4 : 8;
+    static constexpr int kStages = kN == 256 ? 3 : kN == 128 ? 4 : 6;
+    static constexpr int kWStages = kN == 256 ? 3 : 6;
+    // Converter warps: kGroups take the stages in turn; of a stage's two
+    // 64-column halves a warp takes both (kSplit = 1: less to do per stage, and
+    // more stages under way) or one (2: where shared memory holds few stages).
+    static constexpr int kSplit = kN >= 128 ? 2 : 1;
+    static constexpr int kGroups = kConvWarps / (4 * kSplit);
+    // A barrier's phase is told apart by its parity alone, so nobody may wait
+    // for a phase before the one ahead of it is over.  A slot of the code ring
+    // is always the same group's, which has then seen the phase before; a
+    // stage's `empty` is waited for by groups that have written a stage after
+    // the one it frees.
+    static_assert(kWStages % kGroups == 0 && kGroups <= kStages, "phases");
+    static constexpr int kACol0 = kN == 256 ? 256 : 128;  // D before it
     static constexpr int kRing = kStages * kXBytes + kWStages * kWBytes;
     // over half of an SM's: two CTAs there would wait on each other's tensor memory
     static constexpr int kSmem = kRing + 1024 > 116 * 1024 ? kRing + 1024 : 116 * 1024;
-    static_assert(kACol0 + kStages * kACols <= kTmemCols, "tensor memory");
+    static_assert(kN <= kACol0 && kACol0 + kStages * kACols <= kTmemCols, "tensor memory");
     // the cluster's partial sums reuse the rings: chunks of 8 tokens, rounded up per rank
     static_assert((kN / 8 + 7) * 8 * kRows * 4 <= kRing, "partial sums fit the rings");
 };
@@ -171,11 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < G::kWStages; ++i) {
             bar_init(w_full + i, 1);
-            bar_init(w_empty + i, 8);  // a group's converter warps
+            bar_init(w_empty + i, 4 * G::kSplit);  // a group's converter warps
         }
         for (int i = 0; i < G::kStages; ++i) {
             bar_init(x_full + i, 1);
-            bar_init(a_full + i, 8);
+            bar_init(a_full + i, 4 * G::kSplit);
             bar_init(empty + i, 1);  // the MMAs' commit
         }
         bar_init(&done_bar, 1);
@@ -245,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             fence_after();
             const uint64_t b0 = desc_sw128(ring + s * G::kXBytes);
-            const uint32_t acol = tmem + kACol0 + s * kACols;
+            const uint32_t acol = tmem + G::kACol0 + s * kACols;
             if (leader) {
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
@@ -260,53 +272,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (leader) commit(&done_bar);  // all MMAs issued are complete
     } else {
-        // warp (group, half, quarter): rows 32 quarter .. + 31 (lane = row),
-        // columns 64 half .. + 63 of the stages i = group mod kGroups
-        const int quarter = warp & 3, half = (warp >> 2) & 1, group = warp >> 3;
+        // warp (group, half, quarter): rows 32 quarter .. + 31 (lane = row) of
+        // the stages i = group mod kGroups, its half or both
+        constexpr int kHalves = 2 / G::kSplit;
+        const int quarter = warp & 3, half0 = G::kSplit == 2 ? (warp >> 2) & 1 : 0, group = warp / (4 * G::kSplit);
         const int row = min(row0 + quarter * 32 + lane, a.N - 1);
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + kACol0 + half * 32;
         const int r = quarter * 32 + lane;
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + G::kACol0 + half0 * 32;
+        const uint32_t wrow = smem_addr(wring) + r * 64;
+        const int esh = a.stype == kScaleF32 ? 2 : 1;
+        const char* srow = static_cast<const char*>(a.scales) + (((size_t)row * a.G) << esh);
         const bool two = a.gshift == 5;  // two scales for 64 columns
-        const size_t s0 = (size_t)row * a.G;
-        uint32_t raw[2];
+        uint32_t raw[kHalves][2];
         auto load_scales = [&](int i) {
-            const int k = (st0 + i) * kStageK + half * 64;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (u == 1 && !two) break;
-                const size_t at_s = s0 + min((k + 32 * u) >> a.gshift, a.G - 1);
-                raw[u] = a.stype == kScaleF32 ? __ldg(static_cast<const uint32_t*>(a.scales) + at_s)
-                                              : (uint32_t)__ldg(static_cast<const unsigned short*>(a.scales) + at_s);
-            }
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (u == 1 && !two) continue;
+                    const int k = (st0 + i) * kStageK + (half0 + h) * 64 + 32 * u;
+                    const char* p = srow + (min(k >> a.gshift, a.G - 1) << esh);
+                    raw[h][u] = kLow && a.stype == kScaleF32 ? __ldg(reinterpret_cast<const uint32_t*>(p))
+                                                             : (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p));
+                }
         };
-        raw[0] = raw[1] = 0;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) raw[h][0] = raw[h][1] = 0;
         if (group < n) load_scales(group);
-        for (int i = group; i < n; i += kGroups) {
+        for (int i = group; i < n; i += G::kGroups) {
             const int s = i % G::kStages, sw = i % G::kWStages;
-            ScaleParts sp[2];
-            sp[0] = split_scale<kLow>(raw[0], a.stype);
-            sp[1] = two ? split_scale<kLow>(raw[1], a.stype) : sp[0];
-            if (i + kGroups < n) load_scales(i + kGroups);
+            ScaleParts sp[kHalves][2];
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                sp[h][0] = split_scale<kLow>(raw[h][0], a.stype);
+                sp[h][1] = two ? split_scale<kLow>(raw[h][1], a.stype) : sp[h][0];
+            }
+            if (i + G::kGroups < n) load_scales(i + G::kGroups);
             const uint32_t full_ph = (i / G::kWStages) & 1, free_ph = ((i / G::kStages) & 1) ^ 1u;
             // usually both are ready: one round trip to the barriers, not two
             const bool ready = bar_try(w_full + sw, full_ph) & bar_try(empty + s, free_ph);
             if (!__all_sync(0xffffffffu, ready) &&
                 !(warp_wait(w_full + sw, full_ph, abort) && warp_wait(empty + s, free_ph, abort)))
                 break;
-            uint4 w[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)  // 16-byte chunk 2 half + u of the row's 64 bytes (64-byte swizzle)
-                w[u] = lds128(smem_addr(wring) + sw * kWBytes + r * 64 + (((2 * half + u) ^ ((r >> 1) & 3)) << 4));
             fence_after();
-            uint32_t o[32];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                dequant8<kLow>(w[u].x, sp[u], o + 16 * u);
-                dequant8<kLow>(w[u].y, sp[u], o + 16 * u + 4);
-                dequant8<kLow>(w[u].z, sp[u], o + 16 * u + 8);
-                dequant8<kLow>(w[u].w, sp[u], o + 16 * u + 12);
+            for (int h = 0; h < kHalves; ++h) {
+                uint32_t o[32];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {  // 16-byte chunk 2 half + u of the row's 64 bytes (64-byte swizzle)
+                    const uint4 w = lds128(wrow + sw * kWBytes + (((2 * (half0 + h) + u) ^ ((r >> 1) & 3)) << 4));
+                    dequant8<kLow>(w.x, sp[h][u], o + 16 * u);
+                    dequant8<kLow>(w.y, sp[h][u], o + 16 * u + 4);
+                    dequant8<kLow>(w.z, sp[h][u], o + 16 * u + 8);
+                    dequant8<kLow>(w.w, sp[h][u], o + 16 * u + 12);
+                }
+                st_tmem32(at + s * kACols + h * 32, o);
             }
-            st_tmem32(at + s * kACols, o);
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before();
             __syncwarp();
