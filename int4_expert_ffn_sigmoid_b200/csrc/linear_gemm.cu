@@ -154,6 +154,22 @@ __device__ __forceinline__ void dequant8(uint32_t w, const ScaleParts& s, uint32
     }
 }
 
+// A ring's slot and the parity of its phase, stepped instead of divided out:
+// the loading and MMA warps share their schedulers with six converter warps
+// each, and every instruction of theirs waits its turn.
+template <int kSlots>
+struct Slot {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void step(int by = 1) {
+        s += by;
+        if (s >= kSlots) {
+            s -= kSlots;
+            ph ^= 1;
+        }
+    }
+};
+
 struct GemmPlan {
     int stages;  // 128-column stages of a row
     int row_tiles;
@@ -208,56 +224,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const xring = ring_p;
     uint8_t* const wring = ring_p + G::kStages * G::kXBytes;
     if (warp == kWarpW) {
-        if (lane == 0) {  // weights do not depend on the kernel before this one
-            int i = 0;
-            for (; i < n; ++i) {
-                const int s = i % G::kWStages;
-                if (i >= G::kWStages && !bar_wait_or_abort(w_empty + s, (i / G::kWStages - 1) & 1, kWait, abort)) {
-                    *abort = 1;
-                    break;
-                }
-                bar_expect_tx(w_full + s, kWBytes);
-                tma_tile(wring + s * kWBytes, &map_w, w_full + s, (st0 + i) * (kStageK / 2), row0);
+        const bool leader = elect_one();
+        Slot<G::kWStages> w;
+        int i = 0;
+        for (int x = st0 * (kStageK / 2); i < n; ++i, x += kStageK / 2) {  // weights do not depend on the kernel before this one
+            if (i >= G::kWStages && !warp_wait(w_empty + w.s, w.ph ^ 1u, abort)) break;
+            if (leader) {
+                bar_expect_tx(w_full + w.s, kWBytes);
+                tma_tile(wring + w.s * kWBytes, &map_w, w_full + w.s, x, row0);
             }
-            // every copy lands before the CTA's shared memory is reused or goes away
-            for (int j = i > G::kWStages ? i - G::kWStages : 0; j < i; ++j)
-                bar_wait(w_full + j % G::kWStages, (j / G::kWStages) & 1, kWait);
+            w.step();
         }
+        // every copy lands before the CTA's shared memory is reused or goes away
+        for (int j = i > G::kWStages ? i - G::kWStages : 0; j < i; ++j)
+            bar_wait(w_full + j % G::kWStages, (j / G::kWStages) & 1, kWait);
     } else if (warp == kWarpX) {
-        if (lane == 0) {
-            pdl_wait();
-            pdl_release();
-            int i = 0;
-            for (; i < n; ++i) {
-                const int s = i % G::kStages;
-                if (i >= G::kStages && !bar_wait_or_abort(empty + s, (i / G::kStages - 1) & 1, kWait, abort)) {
-                    *abort = 1;
-                    break;
-                }
-                bar_expect_tx(x_full + s, G::kXBytes);
-                uint8_t* x = xring + s * G::kXBytes;
-                tma_tile(x, &map_x, x_full + s, (st0 + i) * kStageK, tok0);
-                tma_tile(x + G::kXBytes / 2, &map_x, x_full + s, (st0 + i) * kStageK + 64, tok0);
+        const bool leader = elect_one();
+        pdl_wait();
+        pdl_release();
+        Slot<G::kStages> t;
+        int i = 0;
+        for (int x = st0 * kStageK; i < n; ++i, x += kStageK) {
+            if (i >= G::kStages && !warp_wait(empty + t.s, t.ph ^ 1u, abort)) break;
+            if (leader) {
+                uint8_t* to = xring + t.s * G::kXBytes;
+                bar_expect_tx(x_full + t.s, G::kXBytes);
+                tma_tile(to, &map_x, x_full + t.s, x, tok0);
+                tma_tile(to + G::kXBytes / 2, &map_x, x_full + t.s, x + 64, tok0);
             }
-            for (int j = i > G::kStages ? i - G::kStages : 0; j < i; ++j)
-                bar_wait(x_full + j % G::kStages, (j / G::kStages) & 1, kWait);
+            t.step();
         }
+        for (int j = i > G::kStages ? i - G::kStages : 0; j < i; ++j)
+            bar_wait(x_full + j % G::kStages, (j / G::kStages) & 1, kWait);
     } else if (warp == kWarpMma) {
         // The whole warp runs the loop and one lane issues: under a divergent
         // `lane == 0` every operand of an MMA is first moved to a uniform
         // register (16 MMAs took 1130 cycles to issue, against 560).
         constexpr uint32_t idesc = idesc_bf16(kRows, kN);
         const bool leader = elect_one();
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const int s = i % G::kStages;
-            const uint32_t ph = (i / G::kStages) & 1;
-            const bool ready = bar_try(x_full + s, ph) & bar_try(a_full + s, ph);
-            ok = __all_sync(0xffffffffu, ready) || (warp_wait(x_full + s, ph, abort) && warp_wait(a_full + s, ph, abort));
-            if (!ok) break;
+        Slot<G::kStages> t;
+        for (int i = 0; i < n; ++i, t.step()) {
+            const bool ready = bar_try(x_full + t.s, t.ph) & bar_try(a_full + t.s, t.ph);
+            if (!__all_sync(0xffffffffu, ready) && !(warp_wait(x_full + t.s, t.ph, abort) && warp_wait(a_full + t.s, t.ph, abort)))
+                break;
             fence_after();
-            const uint64_t b0 = desc_sw128(ring + s * G::kXBytes);
-            const uint32_t acol = tmem + G::kACol0 + s * kACols;
+            const uint64_t b0 = desc_sw128(ring + t.s * G::kXBytes);
+            const uint32_t acol = tmem + G::kACol0 + t.s * kACols;
             if (leader) {
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t b = b0 + ((kb * (G::kXBytes / 2) + kk * 32) >> 4);
                         mma_ts(tmem, acol + kb * 32 + kk * 8, b, idesc, (i | kb | kk) != 0);
                     }
-                commit(empty + s);
+                commit(empty + t.s);
             }
             __syncwarp();
         }
@@ -299,8 +311,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) raw[h][0] = raw[h][1] = 0;
         if (group < n) load_scales(group);
-        for (int i = group; i < n; i += G::kGroups) {
-            const int s = i % G::kStages, sw = i % G::kWStages;
+        Slot<G::kStages> t;
+        Slot<G::kWStages> w;
+        t.step(group);
+        w.step(group);
+        for (int i = group; i < n; i += G::kGroups, t.step(G::kGroups), w.step(G::kGroups)) {
+            const int s = t.s, sw = w.s;
             ScaleParts sp[kHalves][2];
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
@@ -308,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sp[h][1] = two ? split_scale<kLow>(raw[h][1], a.stype) : sp[h][0];
             }
             if (i + G::kGroups < n) load_scales(i + G::kGroups);
-            const uint32_t full_ph = (i / G::kWStages) & 1, free_ph = ((i / G::kStages) & 1) ^ 1u;
+            const uint32_t full_ph = w.ph, free_ph = t.ph ^ 1u;
             // usually both are ready: one round trip to the barriers, not two
             const bool ready = bar_try(w_full + sw, full_ph) & bar_try(empty + s, free_ph);
             if (!__all_sync(0xffffffffu, ready) &&
@@ -320,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t o[32];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {  // 16-byte chunk 2 half + u of the row's 64 bytes (64-byte swizzle)
-                    const uint4 w = lds128(wrow + sw * kWBytes + (((2 * (half0 + h) + u) ^ ((r >> 1) & 3)) << 4));
-                    dequant8<kLow>(w.x, sp[h][u], o + 16 * u);
-                    dequant8<kLow>(w.y, sp[h][u], o + 16 * u + 4);
-                    dequant8<kLow>(w.z, sp[h][u], o + 16 * u + 8);
-                    dequant8<kLow>(w.w, sp[h][u], o + 16 * u + 12);
+                    const uint4 v = lds128(wrow + sw * kWBytes + (((2 * (half0 + h) + u) ^ ((r >> 1) & 3)) << 4));
+                    dequant8<kLow>(v.x, sp[h][u], o + 16 * u);
+                    dequant8<kLow>(v.y, sp[h][u], o + 16 * u + 4);
+                    dequant8<kLow>(v.z, sp[h][u], o + 16 * u + 8);
+                    dequant8<kLow>(v.w, sp[h][u], o + 16 * u + 12);
                 }
                 st_tmem32(at + s * kACols + h * 32, o);
             }
