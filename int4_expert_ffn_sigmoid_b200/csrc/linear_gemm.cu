@@ -15,9 +15,9 @@
 // for 64 tokens x 6144 x 6144, 40.3 against 30.0 for 512 x 4096 x 6144) while
 // the bf16 output's own rounding (1.66e-3) is over twice what it removed.
 //
-// Few row tiles: a cluster of up to eight CTAs shares a tile's columns, sums
-// its parts in shared memory (rank c % size takes tokens 8 c .. 8 c + 7) and
-// stores them; in the same order every time.
+// Few row tiles: a cluster of up to eight CTAs shares a tile's columns; each
+// leaves its part in shared memory and sums all parts of the chunks of eight
+// tokens c = rank mod size, rank 0's first, the same every time.
 //
 // Roles (864 threads, one CTA per SM): warps 0-23 convert (in groups
 // that take the stages in turn) and then read the accumulators out; warps 24
@@ -35,7 +35,6 @@ namespace {
 constexpr int kRows = 128, kStageK = 128;
 constexpr int kConvWarps = 24, kThreads = 32 * (kConvWarps + 3);
 constexpr int kWarpW = kConvWarps, kWarpX = kConvWarps + 1, kWarpMma = kConvWarps + 2;
-constexpr int kColGroups = kConvWarps / 4;  // warps of a lane quarter, for reading the accumulators
 constexpr int kACols = 64;  // tensor memory columns of an A stage
 constexpr int kTmemCols = 512;
 constexpr int kWBytes = kRows * kStageK / 2;
@@ -64,8 +63,7 @@ struct Geo {
     // over half of an SM's: two CTAs there would wait on each other's tensor memory
     static constexpr int kSmem = kRing + 1024 > 116 * 1024 ? kRing + 1024 : 116 * 1024;
     static_assert(kN <= kACol0 && kACol0 + kStages * kACols <= kTmemCols, "tensor memory");
-    // the cluster's partial sums reuse the rings: chunks of 8 tokens, rounded up per rank
-    static_assert((kN / 8 + 7) * 8 * kRows * 4 <= kRing, "partial sums fit the rings");
+    static_assert(kN * kRows * 4 <= kRing, "the f32 tile fits the rings");
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
@@ -353,117 +351,82 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    pdl_wait();  // for every thread that reads add or writes out below (the producer has waited: a no-op there)
+    pdl_wait();  // for every thread that reads add or writes out below (the loading warp has waited: a no-op there)
     __syncwarp();
 
-    // Accumulators to registers: warp (quarter, cgrp): columns 8 c .. + 7, c = cgrp mod kColGroups.
-    constexpr int kChunks = kN / 8, kMine = (kChunks + kColGroups - 1) / kColGroups;
-    const int quarter = warp & 3, cgrp = warp >> 2;
-    float v[kMine][8];
-    auto inside = [&](int t, int row) { return t < a.T && row < a.N; };
-    // Element u of group m of this thread: of its accumulators or, in a
-    // cluster, of the rank's chunks c = rank mod size, a CTA's worth at a time
-    // (at most half as many groups).
-    const int own = (kChunks + size - 1 - rank) / size * 8 * kRows;
-    struct Place {
-        int t, row;
-        bool in;
-    };
-    auto place = [&](int m, int u) {
-        Place p;
-        if (size == 1) {
-            p.t = tok0 + 8 * (cgrp + kColGroups * m) + u;
-            p.row = row0 + quarter * 32 + lane;
-            p.in = cgrp + kColGroups * m < kChunks && inside(p.t, p.row);
-        } else {
-            const int i = threadIdx.x + (8 * m + u) * 32 * kConvWarps;
-            p.t = tok0 + 8 * (i / (8 * kRows) * size + rank) + i / kRows % 8;
-            p.row = row0 + i % kRows;
-            p.in = i < own && inside(p.t, p.row);
-        }
-        return p;
-    };
-    auto load_add = [&](int m, uint16_t (&o)[8]) {
+    // Output i of this CTA (a cluster's rank owns the chunks of eight tokens c =
+    // rank mod size): row i mod 128, token i / 128 of its chunks.  The loops
+    // below are short and rolled: they run once, and code fetched cold costs
+    // more than it does.
+    constexpr int kChunks = kN / 8, kBatch = 4, kStep = 32 * kConvWarps;
+    const int own = (kChunks - rank + size - 1) / size * 8 * kRows;
+    auto token_of = [&](int i) { return (i >> 10) * size * 8 + rank * 8 + ((i >> 7) & 7); };  // of the CTA's tile
+    auto load_add = [&](int i0, uint16_t (&o)[kBatch]) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const Place p = place(m, u);
-            o[u] = a.add && p.in ? __ldcg(reinterpret_cast<const unsigned short*>(a.add) + p.t * a.lda + p.row) : 0;
+        for (int e = 0; e < kBatch; ++e) {
+            const int i = i0 + e * kStep, t = tok0 + token_of(i), row = row0 + (i & 127);
+            o[e] = i < own && t < a.T && row < a.N ? __ldcg(reinterpret_cast<const unsigned short*>(a.add) + t * a.lda + row) : 0;
         }
     };
-    // Up to 128 tokens, add is loaded while the last MMAs run; eight loads at a time otherwise (registers).
-    constexpr int kEarly = kN <= 128 ? kMine : 0;
-    uint16_t plus[kMine][8];
+    uint16_t plus[kBatch] = {};  // on its way while the last MMAs run
+    bool all = false;
     if (warp < kConvWarps) {
-#pragma unroll
-        for (int m = 0; m < kEarly; ++m) load_add(m, plus[m]);
-    }
-    if (warp < kConvWarps) {
+        if (a.add) load_add(threadIdx.x, plus);
         const bool ok = bar_wait(&done_bar, 0, kWait) && *abort == 0 && n > 0;
-        const bool all = __all_sync(0xffffffffu, ok) != 0;
+        all = __all_sync(0xffffffffu, ok) != 0;
         fence_after();
+    }
+    __syncthreads();  // every copy has landed: the rings are free
+    // The tile to shared memory, [token][row].
+    float* tile_sum = reinterpret_cast<float*>(ring_p);
+    if (warp < kConvWarps) {
+        const int quarter = warp & 3;
+#pragma unroll 1
+        for (int c = warp >> 2; c < kChunks; c += kConvWarps / 4) {
+            float v[8];
+            ld_tmem8(tmem + ((uint32_t)(quarter * 32) << 16) + 8 * c, v);
 #pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-            const int c = cgrp + kColGroups * m;
-            if (c < kChunks) ld_tmem8(tmem + ((uint32_t)(quarter * 32) << 16) + 8 * c, v[m]);
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (!all) v[m][u] = __int_as_float(0x7fc00000);
+            for (int u = 0; u < 8; ++u) tile_sum[(c * 8 + u) * kRows + quarter * 32 + lane] = all ? v[u] : __int_as_float(0x7fc00000);
         }
         fence_before();
     }
     __syncthreads();
     // Tensor memory is freed before any wait on another CTA.
     if (warp == kWarpMma) {
-        bar_wait(&done_bar, 0, kWait);
-        __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
     }
-    auto store = [&](int m, const float (&y)[8]) {
-        if (m >= kEarly) load_add(m, plus[m]);
+    if (size > 1) cluster.sync();
+    if (warp < kConvWarps) {
+#pragma unroll 1
+        for (int i0 = threadIdx.x; i0 < own; i0 += kBatch * kStep) {
+            float y[kBatch];
+            uint16_t next[kBatch] = {};
+            if (a.add && i0 + kBatch * kStep < own) load_add(i0 + kBatch * kStep, next);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const Place p = place(m, u);
-            const float o = a.add ? y[u] + bf16lo(plus[m][u]) : y[u];
-            if (!p.in) continue;
-            if (a.out_f32) static_cast<float*>(a.out)[p.t * a.ldo + p.row] = o;
-            else static_cast<__nv_bfloat16*>(a.out)[p.t * a.ldo + p.row] = __float2bfloat16_rn(o);
-        }
-    };
-    if (size == 1) {
-        if (warp < kConvWarps)
+            for (int e = 0; e < kBatch; ++e) y[e] = 0.f;
+#pragma unroll 1
+            for (int q = 0; q < size; ++q) {
+                const float* from = size > 1 ? cluster.map_shared_rank(tile_sum, q) : tile_sum;
 #pragma unroll
-            for (int m = 0; m < kMine; ++m) store(m, v[m]);
-        return;
-    }
-    // [chunk of this rank][source rank][token][row]
-    float* part = reinterpret_cast<float*>(ring_p);
-    cluster.sync();  // every CTA is through with its ring
-    if (warp < kConvWarps)
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-            const int c = cgrp + kColGroups * m;
-            if (c >= kChunks) continue;
-            float* to = cluster.map_shared_rank(part, c % size) + ((size_t)(c / size) * size + rank) * 8 * kRows + quarter * 32 + lane;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) to[u * kRows] = v[m][u];
-        }
-    cluster.sync();
-    if (warp < kConvWarps)
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-            if (8 * m * 32 * kConvWarps >= own) break;
-            float y[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int i = threadIdx.x + (8 * m + u) * 32 * kConvWarps;
-                y[u] = 0.f;
-                if (i < own)
-                    for (int q = 0; q < size; ++q)
-                        y[u] += part[((size_t)(i / (8 * kRows) * size + q) * 8 + i / kRows % 8) * kRows + i % kRows];
+                for (int e = 0; e < kBatch; ++e) {
+                    const int i = i0 + e * kStep;
+                    if (i < own) y[e] += from[token_of(i) * kRows + (i & 127)];
+                }
             }
-            store(m, y);
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int i = i0 + e * kStep, t = tok0 + token_of(i), row = row0 + (i & 127);
+                if (i < own && t < a.T && row < a.N) {
+                    const float o = a.add ? y[e] + bf16lo(plus[e]) : y[e];
+                    if (a.out_f32) static_cast<float*>(a.out)[t * a.ldo + row] = o;
+                    else static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + row] = __float2bfloat16_rn(o);
+                }
+                plus[e] = next[e];
+            }
         }
+    }
+    if (size > 1) cluster.sync();  // no CTA is gone while another reads its tile
 }
 
 struct Capacity {
