@@ -457,14 +457,6 @@ def _scale_shape(rows, cols: int, group: int) -> tuple:
     return (*rows, -(-cols // group)) if group else tuple(rows)
 
 
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _on_device(device: torch.device):
-    """A context in which ``device`` is the current one (calls are short: no switch when it is already)."""
-    return _NO_GUARD if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
-
-
 def _raw_stream(device: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         if stream.device != device:
@@ -510,6 +502,7 @@ class Int4Linear:
         self._w, self._s = w.data_ptr(), scales.data_ptr()
         self.cfg = moe_linear_cfg_t(struct_size=ctypes.sizeof(moe_linear_cfg_t), N=self.N, K=self.K, group=self.group,
                                     scale_type=_scale_type("scales", scales))
+        self._cref, self._index = ctypes.byref(self.cfg), self.device.index
         if lib.moe_linear_kernel_launches(ctypes.byref(self.cfg), 1) == 0:
             raise MoeError(MOE_ERR_UNSUPPORTED, "moe_linear_forward")
 
@@ -517,12 +510,37 @@ class Int4Linear:
                  flags: int = 0, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """out[t] = W x[t] (+ add[t]).  x: bfloat16 [T, K], add: bfloat16 [T, N], out: bfloat16 (float32 under
         MOE_OUT_F32) [T, N]; each may have rows further apart than their length.  ``out`` may be ``add``."""
+        shape, device, cref, ap = x.shape, self.device, self._cref, None
+        T = shape[0]
+        # the common call, without a look at each tensor's strides
+        if not (flags == 0 and out is None and stream is None and x.dtype is torch.bfloat16 and x.get_device() == self._index
+                and x.is_contiguous() and shape == (T, self.K)):
+            return self._general(x, out, add, flags, stream)
+        if add is not None:
+            if not (add.dtype is torch.bfloat16 and add.get_device() == self._index and add.is_contiguous()
+                    and add.shape == (T, self.N)):
+                return self._general(x, out, add, flags, stream)
+            ap = add.data_ptr()
+        if torch._C._cuda_getDevice() != self._index:
+            return self._general(x, out, add, flags, stream)
+        out = x.new_empty(T, self.N)
+        if T == 0:
+            return out
+        st = lib.moe_linear_forward(x.data_ptr(), self._w, self._s, ap, out.data_ptr(), T, cref,
+                                    torch._C._cuda_getCurrentRawStream(self._index))
+        if st != MOE_OK:
+            raise MoeError(st, "moe_linear_forward")
+        return out
+
+    def _general(self, x, out, add, flags, stream):
+        if x.dim() != 2:
+            raise ValueError(f"x: expected [T, {self.K}], got shape {tuple(x.shape)}")
         T, device = x.shape[0], self.device
         odt = torch.float32 if flags & MOE_OUT_F32 else torch.bfloat16
         ldx, ldo, lda, ap = _rows_of("x", x, torch.bfloat16, (T, self.K), device), 0, 0, None
         if out is None:
-            with _NO_GUARD if stream is None else torch.cuda.stream(stream):
-                out = x.new_empty((T, self.N)) if not flags else x.new_empty((T, self.N), dtype=odt)
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                out = x.new_empty((T, self.N), dtype=odt)
         else:
             ldo = _rows_of("out", out, odt, (T, self.N), device)
         if add is not None:
@@ -530,11 +548,9 @@ class Int4Linear:
             ap = add.data_ptr()
         if T == 0:
             return out
-        c = self.cfg
-        if ldx or ldo or lda or flags:
-            c = moe_linear_cfg_t.from_buffer_copy(c)
-            c.ldx, c.ldo, c.lda, c.flags = ldx, ldo, lda, flags
-        with _on_device(device):
+        c = moe_linear_cfg_t.from_buffer_copy(self.cfg)
+        c.ldx, c.ldo, c.lda, c.flags = ldx, ldo, lda, flags
+        with torch.cuda.device(device):
             st = lib.moe_linear_forward(x.data_ptr(), self._w, self._s, ap, out.data_ptr(), T, ctypes.byref(c),
                                         _raw_stream(device, stream))
         if st != MOE_OK:
@@ -607,8 +623,14 @@ class MoEFewLayer:
             keys += [name, sname]
         if any(layer[k].device != self.device for k in keys):
             raise ValueError(f"the layer's tensors are not all on {self.device}")
+        self._tensors = [layer[k] for k in keys]  # their addresses are kept
         self.weights = moe_few_weights_t(**{k: layer[k].data_ptr() for k in keys})
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self.cfg.workspace, self.cfg.workspace_bytes = self.workspace.data_ptr(), n
+        self._add = moe_few_cfg_t.from_buffer_copy(self.cfg)
+        self._add.flags = MOE_ADD_RESIDUAL
+        self._crefs, self._wref, self._index = ((ctypes.byref(self.cfg), ctypes.byref(self._add)),
+                                                ctypes.byref(self.weights), self.device.index)
 
     def new_workspace(self) -> torch.Tensor:
         return torch.empty_like(self.workspace)
@@ -622,21 +644,32 @@ class MoEFewLayer:
                  topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """The layer's output for x (bfloat16 [T, H]); bfloat16 [T, H], float32 under MOE_OUT_F32."""
-        T, shape = x.shape[0], self.shape
+        T = x.shape[0]
+        # the common call, without a configuration of its own
+        if (flags == 0 and out is None and topk_idx is None and topk_w is None and workspace is None and stream is None
+                and x.dtype is torch.bfloat16 and x.get_device() == self._index and x.is_contiguous()
+                and x.shape == (T, self.shape.H) and 0 < T <= self.max_tokens and torch._C._cuda_getDevice() == self._index):
+            out = x.new_empty(T, self.shape.H)
+            st = lib.moe_few_forward(x.data_ptr(), self._wref, out.data_ptr(), T, self._crefs[bool(residual)],
+                                     torch._C._cuda_getCurrentRawStream(self._index))
+            if st != MOE_OK:
+                raise MoeError(st, "moe_few_forward")
+            return out
+        shape = self.shape
         if T > self.max_tokens:
             raise ValueError(f"T={T} exceeds max_tokens={self.max_tokens}")
         f = flags | (MOE_ADD_RESIDUAL if residual else 0)
         odt = torch.float32 if f & MOE_OUT_F32 else torch.bfloat16
-        if out is None:
-            with _NO_GUARD if stream is None else torch.cuda.stream(stream):
-                out = x.new_empty((T, shape.H), dtype=odt)
-        ws = self.workspace if workspace is None else workspace
         self._check("x", x, torch.bfloat16, (T, shape.H))
+        if out is None:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                out = x.new_empty((T, shape.H), dtype=odt)
         self._check("out", out, odt, (T, shape.H))
         if topk_idx is not None:
             self._check("topk_idx", topk_idx, torch.int32, (T, shape.K))
         if topk_w is not None:
             self._check("topk_w", topk_w, torch.float32, (T, shape.K))
+        ws = self.workspace if workspace is None else workspace
         if workspace is not None:
             self._check("workspace", ws, torch.uint8, ws.shape)
         if T == 0:
@@ -646,8 +679,8 @@ class MoEFewLayer:
         c.workspace, c.workspace_bytes = ws.data_ptr(), ws.numel()
         c.topk_idx_out = None if topk_idx is None else topk_idx.data_ptr()
         c.topk_w_out = None if topk_w is None else topk_w.data_ptr()
-        with _on_device(self.device):
-            st = lib.moe_few_forward(x.data_ptr(), ctypes.byref(self.weights), out.data_ptr(), T, ctypes.byref(c),
+        with torch.cuda.device(self.device):
+            st = lib.moe_few_forward(x.data_ptr(), self._wref, out.data_ptr(), T, ctypes.byref(c),
                                      _raw_stream(self.device, stream))
         if st != MOE_OK:
             raise MoeError(st, "moe_few_forward")
