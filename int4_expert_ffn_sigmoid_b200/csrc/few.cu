@@ -7,10 +7,12 @@
 //
 // Both read each touched expert's weights once for all its tokens (group_stream.cuh)
 // and let the columns of an mma tile be the tokens themselves: token t is
-// column pair t of every expert's product, whether it picked the expert or
-// not, so nothing is gathered and the down kernel adds all experts of a row up
-// in registers.  A tile of four tokens that no pick touches is skipped, a
-// token that did not pick the expert is left out of the sum.
+// column pair t % 4 of every expert's product, so the down kernel adds all
+// experts of a row up in registers.  Of tokens q and q + 4 the one that picked
+// the expert takes the column; a second pass over a weight tile is needed only
+// where both did (lane_token; 64 experts of 2560 x 512, 8 of them picked, 8
+// tokens: LATER us, LATER with a pass for each touched half of the tokens).  A
+// column without a token is computed and not used.
 //
 // h is stored as the down kernel's int8 operands: per 32 columns two int8
 // parts and a power-of-two scale (2^-15 of the block's largest value), taken
@@ -82,6 +84,17 @@ __device__ __forceinline__ void few_select(const FewArgs& a, const float* scores
         ssum += s;
     }
     topp_picks(a.K, a.topp, a.scale, lane, my_e, my_s, ssum, out_e, out_w);
+}
+
+// The token of column pair q in a pass over an expert that `tokens` picked; not
+// one of them where the column is unused.
+template <int NT>
+__device__ __forceinline__ int lane_token(unsigned tokens, int q, int pass) {
+    return NT == 1 || (pass == 0 && ((tokens >> q) & 1u)) ? q : q + 4;
+}
+template <int NT>
+__device__ __forceinline__ int token_passes(unsigned tokens) {
+    return NT == 1 || !(tokens & (tokens >> 4)) ? 1 : 2;
 }
 
 template <int NT, bool kCoarse>
@@ -334,14 +347,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         // n-th stage is then never among the last kFewDepth - 1 when it is read.
         for (int i = ahead; i < kFewDepth; ++i) issue();
     }
-    uint32_t xrow[NT];
-    const float* xsc[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int t = min(4 * n + (g >> 1), T - 1);
-        xrow[n] = smem_addr(xq + (2 * t + (g & 1)) * xs_bytes);
-        xsc[n] = xs + min(4 * n + q, T - 1);
-    }
     int slot = 0, parity = 0;
     Tile t;
     if ((int)blockIdx.x >= shared_tiles && (int)blockIdx.x < known) open_scales(tile(blockIdx.x));
@@ -349,7 +354,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     for (int i = blockIdx.x; i < known; i += gridDim.x, parity ^= 1) {
         Tile after = t;
         if (per == 0 && i + (int)gridDim.x < known) after = tile(i + gridDim.x);
-        const unsigned tokens = t.u < 0 ? 0xffu : P.tokens[t.u];
+        const unsigned tokens = t.u < 0 ? (1u << T) - 1 : P.tokens[t.u];
+        const int passes = token_passes<NT>(tokens);
+        uint32_t xrow[NT];
+        const float* xsc[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            xrow[n] = smem_addr(xq + (2 * min(lane_token<NT>(tokens, g >> 1, n), T - 1) + (g & 1)) * xs_bytes);
+            xsc[n] = xs + min(lane_token<NT>(tokens, q, n), T - 1);
+        }
         float acc[NT][2] = {};
         for (int c = j; c < chunks; c += 4) {
             float sc[4];
@@ -364,7 +377,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
             slot = slot == kFewDepth - 1 ? 0 : slot + 1;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if (NT > 1 && !((tokens >> (4 * n)) & 15u)) continue;
+                if (n >= passes) break;
                 const uint32_t xb[1] = {xrow[n] + c * kChunkK};
                 float p[1][2];
                 chunk_mma<1, kCoarse>(st, xb, sc, a.gshift, lane, p);
@@ -378,7 +391,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         float* part = red + parity * kRed;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float* o = part + (warp * 4 * NT + 4 * n + q) * 16;
+            if (n > 0 && !((tokens >> q) & 1u)) continue;  // q + 4 had the first pass
+            float* o = part + (warp * 4 * NT + lane_token<NT>(tokens, q, n)) * 16;
             o[g] = acc[n][0];
             o[g + 8] = acc[n][1];
         }
@@ -543,12 +557,12 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
     const int8_t* hq_shared = a.hq + (size_t)T * a.K * 2 * a.I;
     const float* hs_shared = a.hs + T * a.K * a.I / 32;
     int slot = 0, parity = 0;
-    // This lane's B row (token 4 n + g / 2, part g % 2) and the block scales of
-    // its D columns (token 4 n + q).  A token that did not pick the expert
-    // takes the first that did: its columns' sums are not used.
+    // This lane's B row (the token of column pair g / 2, part g % 2) and the
+    // block scales of its D columns (column pair q).  A column without a token
+    // takes the first token's: its sums are not used.
     auto load_h = [&](const Unit& d, unsigned tokens, int n, uint4 (&x)[4], float4 (&hv)[2]) {
         const int any = __ffs((int)tokens) - 1;
-        int sb = 4 * n + (g >> 1), sd = 4 * n + q;
+        int sb = lane_token<NT>(tokens, g >> 1, n), sd = lane_token<NT>(tokens, q, n);
         if (!((tokens >> sb) & 1u)) sb = any;
         if (!((tokens >> sd) & 1u)) sd = any;
         if (d.u >= 0) {
@@ -577,8 +591,8 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
             const unsigned tokens = d.tokens;
             uint4 x[4];
             float4 hv[2];
-            int n = NT > 1 && !(tokens & 15u) ? 1 : 0;
-            load_h(d, tokens, n, x, hv);
+            const int passes = token_passes<NT>(tokens);
+            load_h(d, tokens, 0, x, hv);
             float sc[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) sc[u] = nsc[u];
@@ -590,11 +604,12 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
             const uint32_t st = ring + slot * kStageBytes;
             slot = slot == kDownDepth - 1 ? 0 : slot + 1;
 #pragma unroll 1
-            for (;;) {
+            for (int n = 0;;) {
                 float t[2];
                 down_mma<kCoarse>(st, x, hv, sc, a.gshift, lane, t);
-                if ((tokens >> (4 * n + q)) & 1u) {
-                    if (NT == 1 || n == 0) {
+                const int tok = lane_token<NT>(tokens, q, n);
+                if (((tokens >> tok) & 1u) && (n == 0 || ((tokens >> q) & 1u))) {  // else: none, or pass 0 had it
+                    if (NT == 1 || tok < 4) {
                         acc[0][0] += t[0];
                         acc[0][1] += t[1];
                     } else {
@@ -602,8 +617,8 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
                         acc[NT - 1][1] += t[1];
                     }
                 }
-                if (NT == 1 || n == 1 || !(tokens >> 4)) break;
-                load_h(d, tokens, n = 1, x, hv);
+                if (NT == 1 || ++n == passes) break;
+                load_h(d, tokens, n, x, hv);
             }
             __syncwarp();
             issue();
