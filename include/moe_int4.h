@@ -388,11 +388,19 @@ int32_t moe_layer_path(const moe_cfg_t* cfg, int32_t T);
  * ceil(n / group) scales, stored row-major [rows][G] (the last group may be
  * short); weight[r][k] = c[r][k] * scale[r][k / group].  group is a power of
  * two from 32 to 32768, or 0 for one scale a row ([rows], the format of
- * moe_layer_forward).  The scales are f32, bf16 or f16 (any finite value,
- * negative and zero ones included).
+ * moe_layer_forward).  The scales are f32, bf16 or f16: zero, or of either
+ * sign with a magnitude from 2^-100 to 2^90 (beyond it partial products leave
+ * f32's range before the sum does; bf16 and f32 scales only).
  *
- * Arithmetic of both operators: f32 sums throughout (except as noted at each
- * entry point), one rounding to bf16 at the end (none under MOE_OUT_F32).
+ * Arithmetic of both operators: f32 sums throughout, one rounding to bf16 at
+ * the end (none under MOE_OUT_F32), the same bits for the same call every
+ * time.  Weight streaming (up to 16 tokens) multiplies the codes with x
+ * rounded to 16 bits, two int8 parts and a power-of-two scale: off by at most
+ * 2^-15 of the largest magnitude of the 256 columns (k / 256) it is in, exact
+ * integer sums within a scale group.  256 columns whose magnitudes are all
+ * below 2^-113 count as zero; a token with a NaN or an infinity gets NaN in
+ * every output.  More tokens run on the bf16 tensor cores: x as it is, each
+ * weight c * scale rounded to bf16 once.
  * ------------------------------------------------------------------------- */
 #define MOE_SCALE_F32 0
 #define MOE_SCALE_BF16 1
@@ -421,8 +429,10 @@ typedef struct moe_linear_cfg {
  * scales are 16-byte aligned, out and add to their element.  The columns of
  * out's rows past N are left as they are.  out must not overlap x, w or
  * scales, and may overlap add only as the same bf16 tensor (same pointer and
- * stride: an in-place update).  No workspace; any number of calls may run at
- * once. */
+ * stride: an in-place update).  A tensor reaches from its first to its last
+ * element: two whose rows lie between one another's count as overlapping.  No
+ * workspace; any number of calls may run at once.  A call whose waits on the
+ * device give up (they are bounded; never in a correct run) leaves NaN. */
 int moe_linear_forward(const void* x, const uint8_t* w, const void* scales, const void* add, void* out, int32_t T,
                        const moe_linear_cfg_t* cfg, void* stream);
 
@@ -479,7 +489,11 @@ int32_t moe_few_pass_tokens(const moe_few_cfg_t* cfg);
 /* Kernels one moe_few_forward call launches (0: T = 0, or rejected). */
 int32_t moe_few_kernel_launches(const moe_few_cfg_t* cfg, int32_t T);
 
-/* x: bf16 [T][H]; out: bf16 [T][H] (f32 under MOE_OUT_F32), not overlapping x;
+/* Weight streaming (see above) for all products; h, with its routing weight
+ * multiplied in, is rounded in the same way over 32 columns each.  The router
+ * is f32 throughout.  A workspace serves one call at a time: streams, and
+ * captured graphs that may run at the same time, have one each.
+ * x: bf16 [T][H]; out: bf16 [T][H] (f32 under MOE_OUT_F32), not overlapping x;
  * T: 0..2^20.  More than moe_few_pass_tokens(cfg) tokens run in passes of that
  * many, each reading its experts' weights again: any T is served, and a call
  * for many tokens belongs to moe_layer_forward (per-row scales). */

@@ -510,8 +510,8 @@ class Int4Linear:
                  flags: int = 0, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """out[t] = W x[t] (+ add[t]).  x: bfloat16 [T, K], add: bfloat16 [T, N], out: bfloat16 (float32 under
         MOE_OUT_F32) [T, N]; each may have rows further apart than their length.  ``out`` may be ``add``."""
-        shape, device, cref, ap = x.shape, self.device, self._cref, None
-        T = shape[0]
+        shape, cref, ap = x.shape, self._cref, None
+        T = shape[0] if shape else -1
         # the common call, without a look at each tensor's strides
         if not (flags == 0 and out is None and stream is None and x.dtype is torch.bfloat16 and x.get_device() == self._index
                 and x.is_contiguous() and shape == (T, self.K)):
@@ -644,6 +644,8 @@ class MoEFewLayer:
                  topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """The layer's output for x (bfloat16 [T, H]); bfloat16 [T, H], float32 under MOE_OUT_F32."""
+        if x.dim() != 2:
+            raise ValueError(f"x: expected [T, {self.shape.H}], got shape {tuple(x.shape)}")
         T = x.shape[0]
         # the common call, without a configuration of its own
         if (flags == 0 and out is None and topk_idx is None and topk_w is None and workspace is None and stream is None

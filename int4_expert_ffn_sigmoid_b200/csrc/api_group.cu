@@ -143,7 +143,10 @@ int32_t moe_few_kernel_launches(const moe_few_cfg_t* cfg, int32_t T) {
     FewArgs a;
     if (few_args(cfg, T, &a) != MOE_OK || T == 0) return 0;
     const int pass = few_pass_tokens(a);
-    return (T + pass - 1) / pass * few_pass_launches(a);
+    int n = T / pass * few_pass_launches(a);  // a.T: the tokens of a full pass
+    a.T = T % pass;
+    if (a.T > 0) n += few_pass_launches(a);
+    return n;
 }
 
 int moe_few_forward(const void* x, const moe_few_weights_t* w, void* out, int32_t T, const moe_few_cfg_t* cfg,

@@ -17,6 +17,15 @@
 // h is stored as the down kernel's int8 operands: per 32 columns two int8
 // parts and a power-of-two scale (2^-15 of the block's largest value), taken
 // in f32 from the finished, routing-weighted h.
+//
+// What bounds it.  256 experts of 6144 x 2048, 8 of them picked, one shared:
+// one token 46.8 us (28.1 at the copy rate), five tokens 185.6 us (120.7).  The
+// gate/up kernel reads at 84 % of the copy rate once its ring is full; the
+// down kernel is held by its instructions (about 300 a warp for 16 rows x 256
+// columns; without the mma products it takes 14 % less, without the loads of h
+// 7 %).  64 experts of 1024 x 512, 2 picked, one token: 10.0 us against 0.95,
+// none of it bandwidth: the chain logits - exchange - selection (1.0) - first
+// routed weights from HBM (1.4) - down (2.4), and two launches.
 #include <cooperative_groups.h>
 
 #include "group_stream.cuh"
@@ -27,21 +36,47 @@ namespace moe {
 constexpr int kFewWarps = 16;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewDepth = 3;
-// The down kernel: more warps, shallower rings.
+// The down kernel: more warps, shallower rings.  Its units are short and each
+// waits for an h from L2, so warps in flight count for more than copies (one
+// token and five of 6144 x 2048, 8 of 256 experts: 46.9 and 185.6 us, 48.7 and
+// 188.7 with 16 warps and rings of three).
 constexpr int kDownWarps = 24, kDownThreads = 32 * kDownWarps, kDownDepth = 2;
 constexpr int kFewTileRows = 32;  // h elements of a gate/up tile
 constexpr int kFewSmemMax = 227 * 1024;
 constexpr int kFewXMax = 98 * 1024;
 // CTAs that share the router: a cluster of kFewCluster computes all logits,
-// each CTA those of a quarter of the experts, and exchanges them in shared
-// memory.  Clusters of four leave 132 of 148 SMs usable, of eight 120.
-// Router weights beyond kFewRouterMax per CTA run as a kernel of their own in
-// front (router_logits_kernel), and every SM takes part in this one.
-constexpr int kFewCluster = 4;
-constexpr int kFewRouterMax = 128 * 1024;
+// each CTA those of an eighth of the experts, and exchanges them in shared
+// memory.  Clusters of eight leave 120 of 148 SMs usable, of four 132, of two
+// all (64 experts of 1024 x 512, one token: 9.4, 9.8 and 10.8 us).  With router
+// weights beyond kFewRouterMax, or gate and up weights beyond kFewWeightsMax
+// (elements of h times H), the logits are a kernel of their own in front
+// (router_logits_kernel) and every SM takes part in this one.  Logits here and
+// in front, us, four tokens:
+//   64 x 1024 router, 192 tiles  12.5, 14.5    1040 tiles of H = 1024  29.6, 32.3 (eight tokens)
+//   64 x 2048, 272 tiles         17.4, 18.9    1024 tiles of H = 2048  36.8, 35.4
+//   64 x 4096, 272 tiles         27.1, 26.7    128 x 4096, 144 tiles   24.3, 20.9
+constexpr int kFewCluster = 8;
+constexpr int kFewRouterMax = 64 * 4096;
+constexpr long long kFewWeightsMax = 40ll << 20;
 
-bool few_split_router(int E, int H) { return (size_t)E * H * 4 > (size_t)kFewCluster * kFewRouterMax; }
 int few_logit_slices(int H) { return (H / 128 + 2) / 3; }
+
+// Shared memory of a gate/up CTA: rings, two buffers of partial sums, scales and
+// int8 parts of x; x itself where the logits are computed here.
+constexpr size_t kFewDynMax = kFewSmemMax - 13 * 1024;  // static shared memory comes on top
+size_t few_smem(int NT, int T, int H, int x_stride, bool split) {
+    const size_t chunks = (H + kChunkK - 1) / kChunkK;
+    return (size_t)kFewWarps * kFewDepth * kStageBytes + 2 * (size_t)kFewWarps * 4 * NT * 16 * 4 + chunks * 4 * NT * 4 +
+           (size_t)2 * T * x_stride + (split ? 0 : (size_t)2 * T * H);
+}
+int few_touched(const FewArgs& a) { return a.E < a.T * a.K ? a.E : a.T * a.K; }
+int few_tiles(const FewArgs& a) { return a.Is / kFewTileRows + few_touched(a) * (a.I / kFewTileRows); }
+// Once true, true for every larger T (a workspace for T tokens serves fewer).
+bool few_split_router(const FewArgs& a) {
+    const int stride = x_stride<true>((a.H + kChunkK - 1) / kChunkK);
+    return a.E * a.H > kFewRouterMax || (long long)few_tiles(a) * kFewTileRows * a.H > kFewWeightsMax ||
+           few_smem(a.T <= 4 ? 1 : 2, a.T, a.H, stride, false) > kFewDynMax;
+}
 
 __device__ __forceinline__ uint32_t ordered(float f) {
     const uint32_t b = __float_as_uint(f);
@@ -195,7 +230,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started
     if (tid < a.E) s_bias[tid] = __ldg(a.rb + tid);
     if (tid < kMaxE / 32) s_mask[tid] = 0;
-    if (tid < kFewMaxU) P.tokens[tid] = 0;
+    // expert 0 for the unused ones: whatever mix of two calls' picks a shared
+    // workspace came to hold would still be experts
+    if (tid < kFewMaxU) P.tokens[tid] = 0, P.expert[tid] = 0;
     if (tid < kFewMaxU * kFewTok) P.slot[tid / kFewTok][tid % kFewTok] = -1;
     static_assert(kFewCluster <= 8, "a lane of eight per CTA");
     static_assert(kFewThreads >= kFewMaxU * kFewTok, "one slot a thread");
@@ -216,14 +253,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     pdl_wait();
     pdl_release();
 
-    // x in shared memory where it fits the room of the partial sums
-    const __nv_bfloat16* x = a.x;
-    const bool staged = a.lslices == 0 && (size_t)T * H * 2 <= 2 * kRed * 4;
-    if (staged) {
-        __nv_bfloat16* xr = reinterpret_cast<__nv_bfloat16*>(red);
+    // x in shared memory, behind its int8 parts, for the logits
+    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(xq + 2 * T * xs_bytes);
+    if (a.lslices == 0) {
+        __nv_bfloat16* xr = const_cast<__nv_bfloat16*>(x);
         for (int i = tid; i < T * H / 8; i += kFewThreads)
             reinterpret_cast<uint4*>(xr)[i] = __ldcg(reinterpret_cast<const uint4*>(a.x) + i);
-        x = xr;
         __syncthreads();
     }
     if (size > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -263,10 +298,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
                     o = fmaf(bf16hi(xv.y), w[i].w, o);
                 }
             };
-            // One token, or all 4 NT of the tile (past the last, it again): four
+            // One or two tokens, or all 4 NT of the tile (past the last, it again):
             // independent chains instead of one after another.
             if (T == 1) {
                 dot(acc[0], xb);
+            } else if (T == 2) {
+                dot(acc[0], xb);
+                dot(acc[1], xb + H / 4);
             } else {
 #pragma unroll
                 for (int t = 0; t < 4 * NT; ++t) dot(acc[t], xb + (size_t)min(t, T - 1) * (H / 4));
@@ -294,10 +332,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     if (size > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
     // int8 activations, while the cluster's other logits arrive
-    if (a.lslices == 0) {
-        if (staged) quantize_tokens<kCoarse, false>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
-        else quantize_tokens<kCoarse, true>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
-    }
+    if (a.lslices == 0)
+        quantize_tokens<kCoarse, false>(x, H, H, chunks, T, xq, xs_bytes, xs, 4 * NT, warp, kFewWarps, lane);
     if (size > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
 
@@ -466,7 +502,7 @@ static_assert(sizeof(Unit) == 24, "packed");
 
 // Down projection of whole output tiles: 16 rows, the shared expert and all
 // touched ones as one long sum, its chunks (units) dealt out to the CTA's
-// warps: unit v to warp v mod 16, the shared expert's chunks first.
+// warps: unit v to warp v mod kDownWarps, the shared expert's chunks first.
 template <int NT, bool kCoarse>
 __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -544,7 +580,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
     for (int i = tid; i < (int)(sizeof(FewPicks) / 4); i += kDownThreads)
         reinterpret_cast<int*>(&P)[i] = __ldcg(reinterpret_cast<const int*>(a.picks) + i);
     __syncthreads();
-    units = Cs + P.U * Ci;
+    units = Cs + min(P.U, T * a.K) * Ci;
     for (int v = Cs + tid; v < units; v += kDownThreads) list[v] = describe(v);
     __syncthreads();
     all = true;
@@ -634,7 +670,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
         if (tid < 16 * T) {
             const int r = tid & 15, t = tid >> 4;
             const size_t o = (size_t)t * a.H + i * 16 + r;
-            float v = a.flags & kFlagResidual ? __bfloat162float(a.x[o]) : 0.f;
+            float v = a.flags & kFlagResidual ? bf16lo(__ldcg(reinterpret_cast<const unsigned short*>(a.x) + o)) : 0.f;
             float y = 0.f;
 #pragma unroll
             for (int w = 0; w < kDownWarps; ++w) y += part[(w * 4 * NT + t) * 16 + r];
@@ -647,11 +683,6 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
 }
 
 namespace {
-
-template <int NT>
-size_t few_smem_base() {
-    return (size_t)kFewWarps * kFewDepth * kStageBytes + 2 * (size_t)kFewWarps * 4 * NT * 16 * 4;
-}
 
 // SMs of the current device, and the CTAs of the gate/up kernel that run at
 // once in clusters of kFewCluster.
@@ -694,31 +725,28 @@ cudaError_t few_launch(const FewArgs& a, cudaStream_t stream) {
     FewDevice& d = devs[dev];
     if (d.clustered == 0) {
         int n = 0, sms = 0;
-        // static shared memory comes on top of the dynamic part
-        constexpr int kMax = kFewSmemMax - 13 * 1024;
-        e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
-        if (e == cudaSuccess) e = few_launch_cluster(up, kFewCluster, kFewCluster, kMax, nullptr, a, &n);
+        e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewDynMax);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewDynMax);
+        if (e == cudaSuccess) e = few_launch_cluster(up, kFewCluster, kFewCluster, kFewDynMax, nullptr, a, &n);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
         if (n <= 0) return cudaErrorInvalidConfiguration;
         d.sms = sms;
         d.clustered = n * kFewCluster;
     }
-    const int chunks = (a.H + kChunkK - 1) / kChunkK;
-    const size_t smem = few_smem_base<NT>() + (size_t)chunks * 4 * NT * 4 + (size_t)2 * a.T * x_stride<kCoarse>(chunks);
+    const size_t smem = few_smem(NT, a.T, a.H, x_stride<kCoarse>((a.H + kChunkK - 1) / kChunkK), a.lslices > 0);
     const int cluster = a.lslices > 0 ? 1 : kFewCluster, most = a.lslices > 0 ? d.sms : d.clustered;
-    const int touched = a.E < a.T * a.K ? a.E : a.T * a.K;
-    const int tiles = a.Is / kFewTileRows + touched * (a.I / kFewTileRows);
+    const int tiles = few_tiles(a);
     int grid = (tiles + cluster - 1) / cluster * cluster;
     if (grid > most) grid = most;
     e = few_launch_cluster(up, grid, cluster, smem, stream, a, nullptr);
     const int out_tiles = a.H / 16;
+    const size_t units = (a.Is + kChunkK - 1) / kChunkK + (size_t)few_touched(a) * ((a.I + kChunkK - 1) / kChunkK);
+    const size_t smem_down = (size_t)kDownWarps * kDownDepth * kStageBytes + 2 * (size_t)kDownWarps * 4 * NT * 16 * 4 +
+                             units * sizeof(Unit);
     if (e == cudaSuccess)
         e = launch_pdl(down, dim3(out_tiles < d.sms ? out_tiles : d.sms), dim3(kDownThreads),
-                       (size_t)kDownWarps * kDownDepth * kStageBytes + 2 * (size_t)kDownWarps * 4 * NT * 16 * 4 + sizeof(Unit) * ((a.Is + kChunkK - 1) / kChunkK +
-                                                            (size_t)touched * ((a.I + kChunkK - 1) / kChunkK)),
-                       stream, a);
+                       smem_down, stream, a);
     return e;
 }
 
@@ -729,7 +757,7 @@ int few_pass_tokens(const FewArgs& a) {
     return fit < kFewTok ? fit : kFewTok;
 }
 
-int few_pass_launches(const FewArgs& a) { return few_split_router(a.E, a.H) ? 3 : 2; }
+int few_pass_launches(const FewArgs& a) { return few_split_router(a) ? 3 : 2; }
 
 size_t few_workspace(FewArgs& a, void* ws) {
     size_t o = 0;
@@ -742,7 +770,7 @@ size_t few_workspace(FewArgs& a, void* ws) {
     a.picks = reinterpret_cast<FewPicks*>(take(sizeof(FewPicks)));
     a.hq = reinterpret_cast<int8_t*>(take(2 * n));
     a.hs = reinterpret_cast<float*>(take(n / 32 * 4));
-    a.lslices = few_split_router(a.E, a.H) ? few_logit_slices(a.H) : 0;
+    a.lslices = few_split_router(a) ? few_logit_slices(a.H) : 0;
     a.lpart = reinterpret_cast<float*>(take((size_t)a.lslices * a.T * a.E * 4));
     return o;
 }

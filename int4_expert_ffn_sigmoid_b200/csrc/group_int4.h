@@ -59,7 +59,6 @@ struct FewArgs {
     int lslices;
 };
 
-
 int linear_launches(const LinearArgs& a);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
 

@@ -4,14 +4,23 @@
 
 namespace moe {
 
-// Weight streaming for up to 16 tokens.  A CTA takes tiles of 16 *
-// wr rows; its warps are wr teams of wk, warp (team, j) multiplying the chunks
+// Weight streaming for up to 16 tokens.  A CTA takes tiles of 16 * wr rows; its warps are wr teams of wk, warp (team, j) multiplying the chunks
 // j, j + wk, ... of its team's 16 rows (chunk_mma) and the team's partial sums
 // meeting in shared memory.  Each warp runs its own ring of kDepth staged
 // chunks on cp.async (no barrier with another warp), across tile borders, and
 // fills it before waiting on the previous kernel: weights and scales are
 // constants, x and add are not.
+//
+// What bounds it: the weights' bytes where there are many (one token x 49152 x
+// 6144: 27.3 us, 88 % of the copy rate), a fixed 4 us of launch, rounding of x,
+// ring fill and drain where there are few (6144 x 6144: 6.7 us, 3.0 at the copy
+// rate; 1024 x 1024: 2.0), and from three tokens on the instructions of the
+// integer products and their scaling (four tokens x 12288 x 6144: 13.8 us, 7.3
+// at the copy rate).  A ring of two or four stages is no faster than three.
 constexpr int kDepth = 3;
+// Tokens at most; more go to the tensor memory GEMM.  16 tokens: 1024 x 1024
+// 4.4 us here, 5.4 there; 2048 x 6144 7.8 and 7.3; 2048 x 12288 10.4 and 8.9.
+// 12 tokens x 2048 x 6144 7.2 and 7.3; 6 x 6144 x 6144 10.3 and 12.8.
 constexpr int kStreamTok = 16;
 // Dynamic shared memory of one CTA at most, and of the activations alone.
 constexpr int kSmemMax = 227 * 1024;
@@ -98,11 +107,13 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
         n = row - team * 16 + (o & (rows_cta - 1));
         return n < a.N;
     };
+    // from L2, as x: the kernel before this one may have written it
+    auto addend = [&](int t, int n) { return bf16lo(__ldcg(reinterpret_cast<const unsigned short*>(a.add) + t * a.lda + n)); };
     for (int i = 0; i < tiles; ++i, row += rows_cta * gridDim.x) {
         float plus = 0.f;  // what the thread's first output is added to: on its way during the products
         if (a.add && tid < outs) {
             int t, n;
-            if (place(tid, t, n)) plus = __bfloat162float(a.add[t * a.lda + n]);
+            if (place(tid, t, n)) plus = addend(t, n);
         }
         float acc[NT][2] = {};
         for (int c = j; c < p.chunks; c += wk) {
@@ -147,7 +158,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel
             const int tm = (o & (rows_cta - 1)) >> 4;
             float v = 0.f;
             for (int u = 0; u < wk; ++u) v += part[(((tm << p.wk_log) + u) * 4 * NT + t) * 16 + (o & 15)];
-            if (a.add) v += o == tid ? plus : __bfloat162float(a.add[t * a.lda + n]);
+            if (a.add) v += o == tid ? plus : addend(t, n);
             if (a.out_f32) static_cast<float*>(a.out)[t * a.ldo + n] = v;
             else static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + n] = __float2bfloat16_rn(v);
         }

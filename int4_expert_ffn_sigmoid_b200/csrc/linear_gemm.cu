@@ -19,10 +19,18 @@
 // leaves its part in shared memory and sums all parts of the chunks of eight
 // tokens c = rank mod size, rank 0's first, the same every time.
 //
-// Roles (864 threads, one CTA per SM): warps 0-23 convert (in groups
-// that take the stages in turn) and then read the accumulators out; warps 24
-// and 25 issue the TMA loads of the codes and of x, warp 26 the MMAs.  Every wait is bounded; a CTA whose wait
-// gave up (never, in a correct run) stores NaN.
+// Roles (864 threads, one CTA per SM): warps 0-23 convert (in groups that take
+// the stages in turn) and then read the accumulators out; warps 24 and 25
+// issue the TMA loads of the codes and of x, warp 26 the MMAs.  Every wait is
+// bounded; a CTA whose wait gave up (never, in a correct run) stores NaN.
+//
+// What bounds it.  64 tokens x 6144 x 6144: 14.6 us (3.4 at the copy rate): the
+// MMAs' pace over the stages of one CTA, 96 of the 148 SMs (48 row tiles in
+// clusters of two), and the start and end of a launch.  512 x 4096 x 6144:
+// 25.2 us, 1.0 PFLOP/s: the loads of x from L2, which each row tile reads anew.
+// Tokens of a tile: the fewest powers of two that hold T, up to 256 (6144 x
+// 6144: 8 tokens 12.9 us, 32 13.2, 128 17.1; a wider tile than T needs costs
+// MMA time and shared memory, a narrower one converts the weights twice).
 #include <cooperative_groups.h>
 #include <cuda.h>
 

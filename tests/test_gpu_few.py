@@ -282,3 +282,37 @@ def test_split_router_passes(moe, cuda_device):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("E,H", [(3, 640), (100, 384), (256, 1024)])
+def test_router_in_the_layer_kernel(moe, cuda_device, T, E, H):
+    """Experts that do not divide among a cluster's CTAs, more than one round of warps, each count of columns."""
+    shape = shape_of(H, E, min(E, 4), 128, 128)
+    assert moe.few_kernel_launches(shape, T, 32) == 2
+    L = make_layer(shape, 32, "f32", seed=E, device=cuda_device)
+    check(moe, tokens(T, shape, L, 40 + T, cuda_device), L, shape, 32)
+
+
+def test_router_placement_differs_by_pass(moe, cuda_device):
+    """A full pass whose x does not fit beside the rings (logits kernel in front), then a short one where it does."""
+    shape = shape_of(4096, 16, 2, 128, 0)
+    assert moe.few_pass_tokens(shape, 128) == 8
+    assert [moe.few_kernel_launches(shape, t, 128) for t in (2, 8, 10, 16)] == [2, 3, 5, 6]
+    sizes = [moe.few_workspace_bytes(shape, t, 128) for t in range(1, 12)]
+    assert sizes == sorted(sizes)
+    L = make_layer(shape, 128, "bf16", device=cuda_device)
+    check(moe, tokens(10, shape, L, 51, cuda_device), L, shape, 128, max_tokens=10)
+
+
+@pytest.mark.parametrize("stype,group", [("bf16", 128), ("f32", 32)])
+def test_tokens_that_share_a_column(moe, cuda_device, stype, group):
+    """Tokens q and q + 4 with the same picks, with one pick in common, and with none."""
+    shape = shape_of(256, 16, 2, 128, 128)
+    L = make_layer(shape, group, stype, seed=3, device=cuda_device)
+    x = tokens(8, shape, L, 61, cuda_device)
+    for other in ([0, 1, 2, 3, 0, 1, 2, 3], [0, 1, 2, 3, 4, 1, 6, 3], [0, 0, 0, 0, 0, 0, 0, 0], list(range(8))):
+        y = x[other].contiguous()
+        out = check(moe, y, L, shape, group)
+        for t, s in enumerate(other):  # equal tokens, equal rows
+            assert torch.equal(out[t], out[other.index(s)])
