@@ -13,7 +13,7 @@ namespace moe {
 //
 // What bounds it: the weights' bytes where there are many (one token x 49152 x
 // 6144: 27.3 us, 88 % of the copy rate), a fixed 4 us of launch, rounding of x,
-// ring fill and drain where there are few (6144 x 6144: 6.7 us, 3.0 at the copy
+// ring fill and drain where there are few (6144 x 6144: 6.5 us, 3.0 at the copy
 // rate; 1024 x 1024: 2.0), and from three tokens on the instructions of the
 // integer products and their scaling (four tokens x 12288 x 6144: 13.8 us, 7.3
 // at the copy rate).  A ring of two or four stages is no faster than three.
@@ -24,7 +24,7 @@ constexpr int kDepth = 3;
 constexpr int kStreamTok = 16;
 // Dynamic shared memory of one CTA at most, and of the activations alone.
 constexpr int kSmemMax = 227 * 1024;
-constexpr int kXMax = 96 * 1024;
+constexpr int kXMax = 98 * 1024;
 
 struct StreamPlan {
     int wk_log, wr_log;  // warps along the columns, teams: 1 << each
@@ -180,10 +180,16 @@ int sms() {
     return cache[dev];
 }
 
+template <int NW, int NT>
+size_t stream_smem(const LinearArgs& a) {
+    const int chunks = (a.K + kChunkK - 1) / kChunkK;
+    return (size_t)NW * kDepth * kStageBytes + 2 * red_floats<NW>(4 * NT) * 4 + (size_t)chunks * 4 * NT * 4 +
+           (size_t)a.T * 2 * (a.gshift >= 7 ? x_stride<true>(chunks) : x_stride<false>(chunks));
+}
+
 template <int NW, int NT, bool kCoarse>
 cudaError_t launch_stream(const LinearArgs& a, StreamPlan p, cudaStream_t stream) {
-    const size_t smem = (size_t)NW * kDepth * kStageBytes + 2 * red_floats<NW>(4 * NT) * 4 + (size_t)p.chunks * 4 * NT * 4 +
-                        (size_t)a.T * 2 * x_stride<kCoarse>(p.chunks);
+    const size_t smem = stream_smem<NW, NT>(a);
     auto* k = linear_stream_kernel<NW, NT, kCoarse>;
     static int set[64];
     int dev = 0;
@@ -192,7 +198,7 @@ cudaError_t launch_stream(const LinearArgs& a, StreamPlan p, cudaStream_t stream
         if (e != cudaSuccess) return e;
         set[dev] = 1;
     }
-    const int per_sm = NW == 8 ? (3 * smem <= kSmemMax - 3 * 1024 ? 3 : 2 * smem <= kSmemMax - 2 * 1024 ? 2 : 1) : 1;
+    const int per_sm = NW == 8 ? 3 : 1;
     p.tiles = (a.N + (16 << p.wr_log) - 1) >> (4 + p.wr_log);
     const int grid = p.tiles < per_sm * sms() ? p.tiles : per_sm * sms();
     return launch_pdl(k, dim3(grid), dim3(32 * NW), smem, stream, a, p);
@@ -221,11 +227,13 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
         p.wr_log = (warps == 8 ? 3 : 4) - p.wk_log;
         return p;
     };
-    // Up to two tokens, eight warps a CTA and three CTAs an SM: the finest
-    // tiles (one token x 1024 x 1024: 2.0 us against 2.2 with 16 warps).  More
-    // tokens: 16 warps share their rounding to int8 (four tokens x 12288 x 6144:
-    // 13.8 us; 24 warps, which leave 80 registers a thread, 14.3).
-    if (a.T <= 2) return launch_stream<8, 1>(a, teams(8), stream);
+    // Up to two tokens and 16 rows an SM: eight warps a CTA, the finest tiles
+    // (one token x 1024 x 1024: 2.0 us against 2.2 with 16 warps; x 512 x 6144:
+    // 3.2 and 3.7).  Otherwise 16 warps share the rounding of x (4096 x 6144: 5.1
+    // us against 5.8; two tokens x 6144 x 6144 6.8 and 8.5; four tokens x 12288
+    // x 6144 13.8, and 14.3 with 24 warps, which leave 80 registers a thread).
+    if (a.T <= 2 && a.N <= 16 * sms() && 3 * stream_smem<8, 1>(a) <= kSmemMax - 3 * 1024)
+        return launch_stream<8, 1>(a, teams(8), stream);
     if (a.T <= 4) return launch_stream<16, 1>(a, teams(16), stream);
     return a.T <= 8 ? launch_stream<16, 2>(a, teams(16), stream) : launch_stream<16, 4>(a, teams(16), stream);
 }
