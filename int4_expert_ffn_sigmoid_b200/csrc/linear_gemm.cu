@@ -28,9 +28,6 @@
 // MMAs' pace over the stages of one CTA, 96 of the 148 SMs (48 row tiles in
 // clusters of two), and the start and end of a launch.  512 x 4096 x 6144:
 // 25.2 us, 1.0 PFLOP/s: the loads of x from L2, which each row tile reads anew.
-// Tokens of a tile: the fewest powers of two that hold T, up to 256 (6144 x
-// 6144: 8 tokens 12.9 us, 32 13.2, 128 17.1; a wider tile than T needs costs
-// MMA time and shared memory, a narrower one converts the weights twice).
 #include <cooperative_groups.h>
 #include <cuda.h>
 
@@ -437,81 +434,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (size > 1) cluster.sync();  // no CTA is gone while another reads its tile
 }
 
-struct Capacity {
-    int ctas[9];  // CTAs of a cluster size that run at once (0: not asked yet)
-};
-
 template <int kN, bool kLow>
-cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
+cudaError_t launch(const LinearArgs& a, int dev, int size, cudaStream_t stream) {
     auto* k = linear_gemm_kernel<kN, kLow>;
     using G = Geo<kN>;
-    static Capacity caps[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static int set[64];
+    cudaError_t e = cudaSuccess;
+    if (!set[dev]) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    cudaLaunchConfig_t c = {};
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = G::kSmem;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    Capacity& cap = caps[dev];
-    if (cap.ctas[1] == 0) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
-        for (int s = 8; s >= 1 && e == cudaSuccess; --s) {
-            int n = 0;
-            at[1].val.clusterDim.x = s;
-            c.gridDim = dim3(s);
-            c.attrs = at + 1;
-            c.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, k, &c);
-            cap.ctas[s] = n * s;
-        }
-        if (e != cudaSuccess) return e;
-    }
+    set[dev] = 1;
     GemmPlan p;
     p.stages = (a.K + kStageK - 1) / kStageK;
     p.row_tiles = (a.N + kRows - 1) / kRows;
-    const long long tiles = (long long)p.row_tiles * ((a.T + kN - 1) / kN);
-    // Columns per cluster: the fewest stages one after another, a CTA's start
-    // and end counted as six stages and the cluster's exchange as six more.
-    int size = 1;
-    long long best = 0;
-    for (int s = 1; s <= 8 && s <= p.stages; ++s) {
-        if (cap.ctas[s] == 0) continue;
-        const long long waves = (tiles * s + cap.ctas[s] - 1) / cap.ctas[s];
-        const long long cost = waves * ((p.stages + s - 1) / s + 6 + (s > 1 ? 6 : 0));
-        if (s == 1 || cost < best) {
-            size = s;
-            best = cost;
-        }
-    }
     CUtensorMap mw, mx;
     if (!encode_tensor_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.w, a.K / 2, a.N, kStageK / 2, kRows,
                               CU_TENSOR_MAP_SWIZZLE_64B) ||
         !encode_tensor_map_rows(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.K, a.T, (uint64_t)a.ldx * 2, 64, kN,
                                 CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    at[1].val.clusterDim.x = size;
-    c.gridDim = dim3((unsigned)(tiles * size));
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)((long long)p.row_tiles * ((a.T + kN - 1) / kN) * size));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = G::kSmem;
     c.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = size;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = 2;
     return cudaLaunchKernelEx(&c, k, mw, mx, a, p);
 }
 
+// CTAs of a cluster size that run at once, of any of the kernels (one an SM).
+struct Capacity {
+    int ctas[9];  // [1] = 0: not asked yet
+};
+cudaError_t capacity(int dev, const Capacity** out) {
+    static Capacity caps[64];
+    Capacity& cap = caps[dev];
+    *out = &cap;
+    if (cap.ctas[1] > 0) return cudaSuccess;
+    auto* k = linear_gemm_kernel<256, true>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<256>::kSmem);
+    for (int s = 8; s >= 1 && e == cudaSuccess; --s) {
+        int n = 0;
+        cudaLaunchConfig_t c = {};
+        c.gridDim = dim3(s);
+        c.blockDim = dim3(kThreads);
+        c.dynamicSmemBytes = Geo<256>::kSmem;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = s;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        c.attrs = &at;
+        c.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, k, &c);
+        cap.ctas[s] = n * s;
+    }
+    return e;
+}
+
+// Time of a CTA, in 10 ns, fitted to 1024 x 1024, 6144 x 6144 and 2048 x 12288
+// (clusters of 8, 2 and 1): stages one after another, start and end, the
+// output of the tile (shared by a cluster), a cluster's exchange.
+struct TileCost {
+    int tokens, stage, fixed, output;
+};
+constexpr TileCost kTiles[] = {{16, 33, 420, 0}, {32, 33, 425, 0}, {64, 36, 500, 10}, {128, 39, 615, 170}, {256, 56, 940, 320}};
+constexpr int kExchange = 80;
+
 }  // namespace
 
+// Tokens of a tile and CTAs of a cluster: the least time of the CTAs' waves by
+// the costs above.  Few rows and many tokens go to narrow tiles, each
+// converting the weights again, many rows to wide ones.  Against the narrowest
+// tile that holds T (up to 256), us: 256 tokens x 1024 x 1024 6.7 and 11.2, 512
+// 7.4 and 14.8, 300 x 6144 x 6144 27.5 and 39.2, 128 x 2048 x 8192 12.6 and
+// 13.3; where the costs mistake the order, 4 % at most was lost.
 cudaError_t launch_linear_gemm(const LinearArgs& a, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const Capacity* cap;
+    if ((e = capacity(dev, &cap)) != cudaSuccess) return e;
+    const int stages = (a.K + kStageK - 1) / kStageK;
+    int tokens = 0, size = 1;
+    long long best = 0;
+    for (const TileCost& c : kTiles) {
+        if (c.tokens >= 2 * a.T && c.tokens > 16) break;
+        const long long tiles = (long long)((a.N + kRows - 1) / kRows) * ((a.T + c.tokens - 1) / c.tokens);
+        for (int s = 1; s <= 8 && s <= stages; ++s) {
+            if (cap->ctas[s] == 0) continue;
+            const long long waves = (tiles * s + cap->ctas[s] - 1) / cap->ctas[s];
+            const long long cost = waves * ((stages + s - 1) / s * c.stage + c.fixed + c.output / s + (s > 1 ? kExchange : 0));
+            if (tokens == 0 || cost < best) {
+                tokens = c.tokens;
+                size = s;
+                best = cost;
+            }
+        }
+    }
     const bool low = a.stype != kScaleBf16;
-    if (a.T <= 16) return low ? launch<16, true>(a, stream) : launch<16, false>(a, stream);
-    if (a.T <= 32) return low ? launch<32, true>(a, stream) : launch<32, false>(a, stream);
-    if (a.T <= 64) return low ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
-    if (a.T <= 128) return low ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
-    return low ? launch<256, true>(a, stream) : launch<256, false>(a, stream);
+    switch (tokens) {
+        case 16: return low ? launch<16, true>(a, dev, size, stream) : launch<16, false>(a, dev, size, stream);
+        case 32: return low ? launch<32, true>(a, dev, size, stream) : launch<32, false>(a, dev, size, stream);
+        case 64: return low ? launch<64, true>(a, dev, size, stream) : launch<64, false>(a, dev, size, stream);
+        case 128: return low ? launch<128, true>(a, dev, size, stream) : launch<128, false>(a, dev, size, stream);
+        default: return low ? launch<256, true>(a, dev, size, stream) : launch<256, false>(a, dev, size, stream);
+    }
 }
 
 }  // namespace moe

@@ -252,3 +252,18 @@ def test_side_stream_tensors(moe, cuda_device):
     got = lin(x, add=a, stream=st)
     st.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("stype,group", [("bf16", 128), ("f32", 32)])
+@pytest.mark.parametrize("T,N,K", [
+    # narrow to wide tiles of tokens, their columns in one CTA or shared out; the last tile of each seldom full
+    (17, 128, 128), (17, 40, 8192), (300, 1000, 416), (20, 6200, 1184), (513, 130, 1184), (256, 130, 2048),
+    (300, 2300, 416), (300, 1000, 1184), (40, 4100, 2048), (170, 500, 4096), (513, 2300, 416), (90, 6200, 4096),
+    (120, 2300, 4096), (513, 4100, 416), (520, 4096, 6144),
+])
+def test_tiles(moe, cuda_device, T, N, K, stype, group):
+    x, w, s, a = make(T, N, K, group, stype, T + N, True, cuda_device)
+    out = moe.Int4Linear(w, s, group)(x, add=a, flags=moe.MOE_OUT_F32)
+    check(out, x, w, s, group, a)
+    want = linear64(x, w, s, group, a)
+    assert float((out.double() - want).norm() / want.norm()) <= linear_rms(T)
