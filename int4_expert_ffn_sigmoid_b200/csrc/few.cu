@@ -57,6 +57,10 @@ constexpr int kFewXMax = 98 * 1024;
 //   64 x 4096, 272 tiles         27.1, 26.7    128 x 4096, 144 tiles   24.3, 20.9
 constexpr int kFewCluster = 8;
 constexpr int kFewRouterMax = 64 * 4096;
+// Columns from which several warps share an expert's logits (six experts of
+// 2688 x 1152, five tokens: 30.6 us, 33.5 with one warp each; where the rows are
+// short the join costs more: 64 x 1024, one token, 10.1 us and 10.6).
+constexpr int kFewShareMin = 2048;
 constexpr long long kFewWeightsMax = 40ll << 20;
 
 int few_logit_slices(int H) { return (H / 128 + 2) / 3; }
@@ -236,16 +240,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     if (tid < kFewMaxU * kFewTok) P.slot[tid / kFewTok][tid % kFewTok] = -1;
     static_assert(kFewCluster <= 8, "a lane of eight per CTA");
     static_assert(kFewThreads >= kFewMaxU * kFewTok, "one slot a thread");
-    // The dot product of this warp's experts e_lo + warp, + 16, ...: eight
-    // 128-column blocks of weights at a time, the next ones on their way.
+    // The dot products of this CTA's experts.  Of eight experts and fewer, with
+    // rows of 16 blocks of 128 columns and more, 1 << plog warps share each one's
+    // blocks (b_lo .. b_hi - 1 are this warp's); else a warp has experts of its
+    // own.  Eight blocks of weights at a time, the next ones on their way.
+    int plog = 0;
+    while (H >= kFewShareMin && (epc << (plog + 1)) <= kFewWarps) ++plog;
+    const int teams = kFewWarps >> plog, part = warp & ((1 << plog) - 1);
+    const int b_lo = (H / 128 * part) >> plog, b_hi = (H / 128 * (part + 1)) >> plog;
     float4 wn[8];
     auto load_w = [&](int e, int b) {
         const float4* w = reinterpret_cast<const float4*>(a.rw + (size_t)e * H) + lane;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wn[i] = b + i < H / 128 ? __ldg(w + (b + i) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 8; ++i) wn[i] = b + i < b_hi ? __ldg(w + (b + i) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    int e = a.lslices > 0 ? e_hi : e_lo + warp;
-    if (e < e_hi) load_w(e, 0);
+    int e = a.lslices > 0 ? e_hi : e_lo + (warp >> plog);
+    if (e < e_hi) load_w(e, b_lo);
     // Behind the logits kernel x is final: that kernel let this one start only
     // after its own wait for whatever wrote x.
     if (a.lslices > 0)
@@ -268,30 +278,34 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
         for (int i = tid; i < T * a.E; i += kFewThreads) {  // no cluster then: every CTA sums all of them
             const float* l = a.lpart + i;
             float v = 0.f;
-#pragma unroll 8
-            for (int s = 0; s < a.lslices; ++s) v += __ldcg(l + (size_t)s * T * a.E);
+            for (int s0 = 0; s0 < a.lslices; s0 += 8) {  // eight loads on their way, whatever the count
+                float p[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s) p[s] = s0 + s < a.lslices ? __ldcg(l + (size_t)(s0 + s) * T * a.E) : 0.f;
+#pragma unroll
+                for (int s = 0; s < 8; ++s) v += p[s];
+            }
             s_logit[i / a.E][i % a.E] = v;
         }
     } else {
         float acc[4 * NT] = {};
-        for (int b = 0; e < e_hi;) {
+        for (int b = b_lo; e < e_hi;) {
             float4 w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = wn[i];
-            const int e_now = e, nb = min(8, H / 128 - b);
+            const int e_now = e, nb = min(8, b_hi - b);
             const uint2* xb = reinterpret_cast<const uint2*>(x + b * 128) + lane;
             b += 8;
-            const bool last = b >= H / 128;
+            const bool last = b >= b_hi;
             if (last) {
-                b = 0;
-                e += kFewWarps;
+                b = b_lo;
+                e += teams;
             }
             if (e < e_hi) load_w(e, b);
             auto dot = [&](float& o, const uint2* xt) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (i >= nb) break;
-                    const uint2 xv = xt[i * 32];
+                    const uint2 xv = i < nb ? xt[i * 32] : make_uint2(0, 0);
                     o = fmaf(bf16lo(xv.x), w[i].x, o);
                     o = fmaf(bf16hi(xv.x), w[i].y, o);
                     o = fmaf(bf16lo(xv.y), w[i].z, o);
@@ -324,8 +338,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 const int t = 4 * n + (lane >> 3);
-                if (t < T && (lane & 7) < size) *cluster.map_shared_rank(&s_logit[t][e_now], lane & 7) = s;
+                if (plog == 0) {
+                    if (t < T && (lane & 7) < size) *cluster.map_shared_rank(&s_logit[t][e_now], lane & 7) = s;
+                } else if (t < T && (lane & 7) == 0) {
+                    red[(((e_now - e_lo) << plog) + part) * kFewTok + t] = s;
+                }
                 v[0] = v[1] = v[2] = v[3] = 0.f;
+            }
+        }
+        if (plog > 0) {  // added up, and sent to every CTA of the cluster
+            __syncthreads();
+            const int t = (tid >> 3) & 7, le = tid >> 6;
+            static_assert(kFewTok == 8 && kFewCluster == 8 && kFewThreads >= 8 * 64, "a thread per token, rank and expert of eight");
+            if (le < e_hi - e_lo && t < T && (tid & 7) < size) {
+                float v = 0.f;
+                for (int k = 0; k < 1 << plog; ++k) v += red[((le << plog) + k) * kFewTok + t];
+                *cluster.map_shared_rank(&s_logit[t][e_lo + le], tid & 7) = v;
             }
         }
     }
