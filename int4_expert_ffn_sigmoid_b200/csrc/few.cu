@@ -19,11 +19,11 @@
 // in f32 from the finished, routing-weighted h.
 //
 // What bounds it.  256 experts of 6144 x 2048, 8 of them picked, one shared:
-// one token 46.8 us (28.1 at the copy rate), five tokens 185.6 us (120.7).  The
-// gate/up kernel reads at 84 % of the copy rate once its ring is full; the
-// down kernel is held by its instructions (about 300 a warp for 16 rows x 256
-// columns; without the mma products it takes 14 % less, without the loads of h
-// 7 %).  64 experts of 1024 x 512, 2 picked, one token: 10.0 us against 0.95,
+// one token 46.8 us (28.1 at the copy rate), five tokens 185.6 us (120.7).  Both
+// kernels are held by their instructions (59 and 67 % of the issue slots at
+// five tokens, 49 and 33 % of DRAM's peak): about 300 a warp for 16 rows x 256
+// columns of the down kernel, of whose time the mma products take 14 % and the
+// loads of h 7 %.  64 experts of 1024 x 512, 2 picked, one token: 10.0 us against 0.95,
 // none of it bandwidth: the chain logits - exchange - selection (1.0) - first
 // routed weights from HBM (1.4) - down (2.4), and two launches.
 #include <cooperative_groups.h>
