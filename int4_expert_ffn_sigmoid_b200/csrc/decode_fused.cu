@@ -841,6 +841,7 @@ __device__ void producer(const FArgs& a, Sh& sh, uint8_t* wring, uint8_t* xring,
                 int s, round;
                 if (!acquire(s, round)) { ok = false; break; }
                 if (lane == 0) {
+                    refill_fence();
                     bar_expect_tx(&sh.full[s], kTmaWBytes);
                     tma_tile(wring + (size_t)s * kTmaWBytes, tms13, &sh.full[s], npre * kTmaRowBytes, rg);
                     tma_tile(wring + (size_t)s * kTmaWBytes + kTmaWBytes / 2, tms13, &sh.full[s], npre * kTmaRowBytes,
@@ -885,6 +886,7 @@ __device__ void producer(const FArgs& a, Sh& sh, uint8_t* wring, uint8_t* xring,
                     int round;
                     if (!acquire(s, round)) { ok = false; break; }
                     if (lane == 0) {
+                        refill_fence();
                         bar_expect_tx(&sh.full[s], kTmaWBytes);
                         tma_tile(wring + (size_t)s * kTmaWBytes, map, &sh.full[s], c * kTmaRowBytes, rg);
                         tma_tile(wring + (size_t)s * kTmaWBytes + kTmaWBytes / 2, map, &sh.full[s], c * kTmaRowBytes,
@@ -922,6 +924,7 @@ __device__ void producer(const FArgs& a, Sh& sh, uint8_t* wring, uint8_t* xring,
                     int s, round;
                     if (!acquire(s, round)) { ok = false; break; }
                     if (lane == 0) {
+                        refill_fence();
                         bar_expect_tx(&sh.full[s], kW2Bytes);
                         tma_tile(wring + (size_t)s * kTmaWBytes, map, &sh.full[s], (k0 + c * kTmaChunk) / 2,
                                  row0 + m * kTaskRows2);

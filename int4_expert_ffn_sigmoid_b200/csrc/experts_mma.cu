@@ -682,6 +682,7 @@ __device__ __forceinline__ void issue13(const Params& p, const Task13& t, uint8_
     const size_t rb = (size_t)p.H / 2;
     const uint8_t* W = t.shared ? p.sh_w13 : p.w13 + (size_t)t.e * 2 * p.I * rb;
     const int r0 = t.r0;  // this warp's first row (r0 is per warp)
+    refill_fence();
     bar_expect_tx(bar, (uint32_t)(16 * rb));
     bulk_g2s(slot, W + (size_t)r0 * rb, (uint32_t)(8 * rb), bar);
     bulk_g2s(slot + 8 * rb, W + (size_t)(t.irow + r0) * rb, (uint32_t)(8 * rb), bar);
@@ -882,6 +883,7 @@ template <int WB>
 __device__ __forceinline__ void issue_w13_chunk(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int c, int rg,
                                                 int ru) {
     constexpr int kTile = kRows13 * kTmaRowBytes;
+    refill_fence();
     bar_expect_tx(bar, kTmaWBytes * WB / 4);
     if (WB == 4) {
         tma_tile(dst, map, bar, c * kTmaRowBytes, rg);
@@ -1885,6 +1887,7 @@ __device__ __forceinline__ void consume2(const Task2& tk, uint32_t& n, uint64_t*
 // tile of int4, two of int8.
 template <int WB>
 __device__ __forceinline__ void issue_w2_chunk(const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int k0, int row) {
+    refill_fence();
     bar_expect_tx(bar, kW2Bytes * WB / 4);
     if (WB == 4) {
         tma_tile(dst, map, bar, k0 / 2, row);

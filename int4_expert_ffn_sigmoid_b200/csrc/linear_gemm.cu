@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = st0 * (kStageK / 2); i < n; ++i, x += kStageK / 2) {  // weights do not depend on the kernel before this one
             if (i >= G::kWStages && !warp_wait(w_empty + w.s, w.ph ^ 1u, abort)) break;
             if (leader) {
+                refill_fence();
                 bar_expect_tx(w_full + w.s, kWBytes);
                 tma_tile(wring + w.s * kWBytes, &map_w, w_full + w.s, x, row0);
             }
