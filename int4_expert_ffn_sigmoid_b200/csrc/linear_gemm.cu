@@ -360,24 +360,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();  // for every thread that reads add or writes out below (the loading warp has waited: a no-op there)
     __syncwarp();
 
-    // Output i of this CTA (a cluster's rank owns the chunks of eight tokens c =
-    // rank mod size): row i mod 128, token i / 128 of its chunks.  The loops
-    // below are short and rolled: they run once, and code fetched cold costs
-    // more than it does.
-    constexpr int kChunks = kN / 8, kBatch = 4, kStep = 32 * kConvWarps;
-    const int own = (kChunks - rank + size - 1) / size * 8 * kRows;
-    auto token_of = [&](int i) { return (i >> 10) * size * 8 + rank * 8 + ((i >> 7) & 7); };  // of the CTA's tile
-    auto load_add = [&](int i0, uint16_t (&o)[kBatch]) {
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-            const int i = i0 + e * kStep, t = tok0 + token_of(i), row = row0 + (i & 127);
-            o[e] = i < own && t < a.T && row < a.N ? __ldcg(reinterpret_cast<const unsigned short*>(a.add) + t * a.lda + row) : 0;
-        }
+    // Output u of this CTA (a cluster's rank owns the chunks of eight tokens c =
+    // rank mod size): one token's 128 rows, a warp each, four rows a lane.  The
+    // loops below are short and rolled: they run once, and code fetched cold
+    // costs more than it does.
+    constexpr int kChunks = kN / 8, kBatch = 2;
+    const int own = (kChunks - rank + size - 1) / size * 8;
+    auto token_of = [&](int u) { return (u >> 3) * size * 8 + rank * 8 + (u & 7); };  // of the CTA's tile
+    const int row = row0 + 4 * lane;
+    const bool four = row + 3 < a.N;
+    const bool add4 = four && a.lda % 4 == 0 && reinterpret_cast<uintptr_t>(a.add) % 8 == 0;
+    const bool out4 = four && a.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.out_f32 ? 16 : 8) == 0;
+    auto load_add = [&](int u) {  // four bf16
+        const int t = tok0 + token_of(u);
+        uint2 o = make_uint2(0, 0);
+        if (u >= own || t >= a.T) return o;
+        const unsigned short* p = reinterpret_cast<const unsigned short*>(a.add) + t * a.lda + row;
+        if (add4) return __ldcg(reinterpret_cast<const uint2*>(p));
+        if (row < a.N) o.x = __ldcg(p);
+        if (row + 1 < a.N) o.x |= (uint32_t)__ldcg(p + 1) << 16;
+        if (row + 2 < a.N) o.y = __ldcg(p + 2);
+        if (four) o.y |= (uint32_t)__ldcg(p + 3) << 16;
+        return o;
     };
-    uint16_t plus[kBatch] = {};  // on its way while the last MMAs run
+    uint2 plus[kBatch] = {};  // on its way while the last MMAs run
     bool all = false;
     if (warp < kConvWarps) {
-        if (a.add) load_add(threadIdx.x, plus);
+        if (a.add)
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) plus[e] = load_add(warp + e * kConvWarps);
         const bool ok = bar_wait(&done_bar, 0, kWait) && *abort == 0 && n > 0;
         all = __all_sync(0xffffffffu, ok) != 0;
         fence_after();
@@ -405,28 +416,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (size > 1) cluster.sync();
     if (warp < kConvWarps) {
 #pragma unroll 1
-        for (int i0 = threadIdx.x; i0 < own; i0 += kBatch * kStep) {
-            float y[kBatch];
-            uint16_t next[kBatch] = {};
-            if (a.add && i0 + kBatch * kStep < own) load_add(i0 + kBatch * kStep, next);
+        for (int u0 = warp; u0 < own; u0 += kBatch * kConvWarps) {
+            float4 y[kBatch];
+            uint2 next[kBatch] = {};
+            if (a.add)
 #pragma unroll
-            for (int e = 0; e < kBatch; ++e) y[e] = 0.f;
+                for (int e = 0; e < kBatch; ++e) next[e] = load_add(u0 + (kBatch + e) * kConvWarps);
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
             for (int q = 0; q < size; ++q) {
-                const float* from = size > 1 ? cluster.map_shared_rank(tile_sum, q) : tile_sum;
+                const float* from = (size > 1 ? cluster.map_shared_rank(tile_sum, q) : tile_sum) + 4 * lane;
 #pragma unroll
                 for (int e = 0; e < kBatch; ++e) {
-                    const int i = i0 + e * kStep;
-                    if (i < own) y[e] += from[token_of(i) * kRows + (i & 127)];
+                    const int u = u0 + e * kConvWarps;
+                    if (u >= own) continue;
+                    const float4 v = *reinterpret_cast<const float4*>(from + token_of(u) * kRows);
+                    y[e].x += v.x;
+                    y[e].y += v.y;
+                    y[e].z += v.z;
+                    y[e].w += v.w;
                 }
             }
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
-                const int i = i0 + e * kStep, t = tok0 + token_of(i), row = row0 + (i & 127);
-                if (i < own && t < a.T && row < a.N) {
-                    const float o = a.add ? y[e] + bf16lo(plus[e]) : y[e];
-                    if (a.out_f32) static_cast<float*>(a.out)[t * a.ldo + row] = o;
-                    else static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + row] = __float2bfloat16_rn(o);
+                const int u = u0 + e * kConvWarps, t = tok0 + token_of(u);
+                if (u < own && t < a.T) {
+                    float o[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+                    if (a.add) {
+                        o[0] += bf16lo(plus[e].x);
+                        o[1] += bf16hi(plus[e].x);
+                        o[2] += bf16lo(plus[e].y);
+                        o[3] += bf16hi(plus[e].y);
+                    }
+                    if (a.out_f32) {
+                        float* to = static_cast<float*>(a.out) + t * a.ldo + row;
+                        if (out4) {
+                            *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (row + i < a.N) to[i] = o[i];
+                        }
+                    } else {
+                        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + row;
+                        if (out4) {
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+                            *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                                       *reinterpret_cast<const uint32_t*>(&hi));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (row + i < a.N) to[i] = __float2bfloat16_rn(o[i]);
+                        }
+                    }
                 }
                 plus[e] = next[e];
             }
