@@ -24,10 +24,12 @@
 // issue the TMA loads of the codes and of x, warp 26 the MMAs.  Every wait is
 // bounded; a CTA whose wait gave up (never, in a correct run) stores NaN.
 //
-// What bounds it.  64 tokens x 6144 x 6144: 14.6 us (3.4 at the copy rate): the
+// What bounds it.  64 tokens x 6144 x 6144: 13.9 us (3.4 at the copy rate): the
 // MMAs' pace over the stages of one CTA, 96 of the 148 SMs (48 row tiles in
 // clusters of two), and the start and end of a launch.  512 x 4096 x 6144:
-// 25.2 us, 1.0 PFLOP/s: the loads of x from L2, which each row tile reads anew.
+// 22.5 us, 1.15 PFLOP/s: in its 24 stages a CTA's MMAs run at their full rate
+// (1024 cycles each, 13 us); the first stage's loads and conversion, the
+// cluster's exchange and the output take the rest, and 20 SMs have no tile.
 #include <cooperative_groups.h>
 #include <cuda.h>
 
@@ -541,23 +543,25 @@ cudaError_t capacity(int dev, const Capacity** out) {
     return e;
 }
 
-// Time of a CTA, in 10 ns, fitted to 1024 x 1024, 6144 x 6144 and 2048 x 12288
-// (clusters of 8, 2 and 1): stages one after another, start and end, the
-// output of the tile (shared by a cluster), a cluster's exchange.
+// Time of a CTA, in 10 ns: its stages one after another, its start and end, a
+// cluster's exchange, and what a launch takes that leaves the next one less
+// than half of the SMs to start on while it runs.  Fitted (8 % r.m.s.) to 1330
+// measured launches of 11 shapes from 256 x 1024 to 12288 x 2048, 20 to 512
+// tokens, each tile width and cluster size, one after another on a stream.
 struct TileCost {
-    int tokens, stage, fixed, output;
+    int tokens, stage, fixed;
 };
-constexpr TileCost kTiles[] = {{16, 33, 420, 0}, {32, 33, 425, 0}, {64, 36, 500, 10}, {128, 39, 615, 170}, {256, 56, 940, 320}};
-constexpr int kExchange = 80;
+constexpr TileCost kTiles[] = {{16, 36, 160}, {32, 36, 184}, {64, 36, 257}, {128, 39, 379}, {256, 56, 648}};
+constexpr int kExchange = 53, kExchangeCta = 29, kCrowd = 200;
 
 }  // namespace
 
 // Tokens of a tile and CTAs of a cluster: the least time of the CTAs' waves by
-// the costs above.  Few rows and many tokens go to narrow tiles, each
-// converting the weights again, many rows to wide ones.  Against the narrowest
-// tile that holds T (up to 256), us: 256 tokens x 1024 x 1024 6.7 and 11.2, 512
-// 7.4 and 14.8, 300 x 6144 x 6144 27.5 and 39.2, 128 x 2048 x 8192 12.6 and
-// 13.3; where the costs mistake the order, 4 % at most was lost.
+// the costs above, which is within 2 % of the best of all on average (35 % at
+// worst).  Few rows and many tokens go to narrow tiles, each converting the
+// weights again, many rows to wide ones.  Against the narrowest tile that holds
+// T (up to 256), us: 64 tokens x 1024 x 1024 3.7 and 6.2, 256 4.3 and 11.2, 300 x
+// 6144 x 6144 27 and 39, 40 x 2048 x 8192 9.4 and 12.5.
 cudaError_t launch_linear_gemm(const LinearArgs& a, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -573,8 +577,9 @@ cudaError_t launch_linear_gemm(const LinearArgs& a, cudaStream_t stream) {
         const long long tiles = (long long)((a.N + kRows - 1) / kRows) * ((a.T + c.tokens - 1) / c.tokens);
         for (int s = 1; s <= 8 && s <= stages; ++s) {
             if (cap->ctas[s] == 0) continue;
-            const long long waves = (tiles * s + cap->ctas[s] - 1) / cap->ctas[s];
-            const long long cost = waves * ((stages + s - 1) / s * c.stage + c.fixed + c.output / s + (s > 1 ? kExchange : 0));
+            const long long ctas = tiles * s, waves = (ctas + cap->ctas[s] - 1) / cap->ctas[s];
+            const long long cost = waves * ((stages + s - 1) / s * c.stage + c.fixed + (s > 1 ? kExchange + kExchangeCta * s : 0)) +
+                                   (2 * ctas > cap->ctas[1] ? kCrowd : 0);
             if (tokens == 0 || cost < best) {
                 tokens = c.tokens;
                 size = s;
