@@ -267,3 +267,23 @@ def test_tiles(moe, cuda_device, T, N, K, stype, group):
     check(out, x, w, s, group, a)
     want = linear64(x, w, s, group, a)
     assert float((out.double() - want).norm() / want.norm()) <= linear_rms(T)
+
+
+@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("N", [128, 130, 1003])
+def test_wide_stores(moe, cuda_device, T, N):
+    """Rows on 8- and 16-byte borders, with a last piece of rows that is not whole; f32 and bf16 outputs."""
+    K, group = 1024, 128
+    x, w, s, a = make(T, N, K, group, "bf16", 6, True, cuda_device)
+    lin = moe.Int4Linear(w, s, group)
+    wide = (N + 7) // 4 * 4
+    aw = torch.full((T, wide), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+    aw[:, :N] = a
+    for flags, dtype in ((0, torch.bfloat16), (moe.MOE_OUT_F32, torch.float32)):
+        for at in (0, 1):  # on a border, and beside it
+            buf = torch.full((T * wide + 8,), 7.0, dtype=dtype, device=cuda_device)
+            out = buf[at:at + T * wide].view(T, wide)[:, :N]
+            lin(x, out=out, add=aw[:, :N], flags=flags)
+            check(out, x, w, s, group, a)
+            assert bool((buf[at:at + T * wide].view(T, wide)[:, N:] == 7).all())
+            assert bool((buf[:at] == 7).all()) and bool((buf[at + T * wide:] == 7).all())
