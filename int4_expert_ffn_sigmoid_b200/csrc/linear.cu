@@ -227,12 +227,13 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
         p.wr_log = (warps == 8 ? 3 : 4) - p.wk_log;
         return p;
     };
-    // Up to two tokens and 16 rows an SM: eight warps a CTA, the finest tiles
-    // (one token x 1024 x 1024: 2.0 us against 2.2 with 16 warps; x 512 x 6144:
-    // 3.2 and 3.7).  Otherwise 16 warps share the rounding of x (4096 x 6144: 5.1
-    // us against 5.8; two tokens x 6144 x 6144 6.8 and 8.5; four tokens x 12288
-    // x 6144 13.8, and 14.3 with 24 warps, which leave 80 registers a thread).
-    if (a.T <= 2 && a.N <= 16 * sms() && 3 * stream_smem<8, 1>(a) <= kSmemMax - 3 * 1024)
+    // Up to four tokens and 16 rows an SM: eight warps a CTA, the finest tiles,
+    // and room for the next launch to start beside it (1024 x 1024, one token 2.0
+    // us against 2.2 with 16 warps, four 2.2 and 2.5; one x 512 x 6144 3.2 and
+    // 3.7).  Otherwise 16 warps share the rounding of x (4096 x 6144: 5.1 us against
+    // 5.8; two tokens x 6144 x 6144 6.8 and 8.5; four tokens x 12288 x 6144 13.8,
+    // and 14.3 with 24 warps, which leave 80 registers a thread).
+    if (a.T <= 4 && a.N <= 16 * sms() && 3 * stream_smem<8, 1>(a) <= kSmemMax - 3 * 1024)
         return launch_stream<8, 1>(a, teams(8), stream);
     if (a.T <= 4) return launch_stream<16, 1>(a, teams(16), stream);
     return a.T <= 8 ? launch_stream<16, 2>(a, teams(16), stream) : launch_stream<16, 4>(a, teams(16), stream);
