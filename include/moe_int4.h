@@ -394,7 +394,8 @@ int32_t moe_layer_path(const moe_cfg_t* cfg, int32_t T);
  *
  * Arithmetic of both operators: f32 sums throughout, one rounding to bf16 at
  * the end (none under MOE_OUT_F32), the same bits for the same call every
- * time.  Weight streaming (up to 16 tokens) multiplies the codes with x
+ * time.  Weight streaming (up to eight tokens, fewer where rows are long and
+ * few) multiplies the codes with x
  * rounded to 16 bits, two int8 parts and a power-of-two scale: off by at most
  * 2^-15 of the largest magnitude of the 256 columns (k / 256) it is in, exact
  * integer sums within a scale group.  256 columns whose magnitudes are all

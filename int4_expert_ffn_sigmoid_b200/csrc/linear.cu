@@ -4,8 +4,9 @@
 
 namespace moe {
 
-// Weight streaming for up to 16 tokens.  A CTA takes tiles of 16 * wr rows; its warps are wr teams of wk, warp (team, j) multiplying the chunks
-// j, j + wk, ... of its team's 16 rows (chunk_mma) and the team's partial sums
+// Weight streaming for up to eight tokens.  A CTA takes tiles of 16 * wr rows;
+// its warps are wr teams of wk, warp (team, j) multiplying the chunks j, j +
+// wk, ... of its team's 16 rows (chunk_mma) and the team's partial sums
 // meeting in shared memory.  Each warp runs its own ring of kDepth staged
 // chunks on cp.async (no barrier with another warp), across tile borders, and
 // fills it before waiting on the previous kernel: weights and scales are
@@ -18,13 +19,18 @@ namespace moe {
 // integer products and their scaling (four tokens x 12288 x 6144: 13.8 us, 7.3
 // at the copy rate).  A ring of two or four stages is no faster than three.
 constexpr int kDepth = 3;
-// Tokens at most; more go to the tensor memory GEMM.  16 tokens: 1024 x 1024
-// 4.4 us here, 5.4 there; 2048 x 6144 7.8 and 7.3; 2048 x 12288 10.4 and 8.9.
-// 12 tokens x 2048 x 6144 7.2 and 7.3; 6 x 6144 x 6144 10.3 and 12.8.
-constexpr int kStreamTok = 16;
-// Dynamic shared memory of one CTA at most, and of the activations alone.
+// Dynamic shared memory of one CTA at most, and of the activations alone
+// (eight tokens of 7168 columns).
 constexpr int kSmemMax = 227 * 1024;
-constexpr int kXMax = 98 * 1024;
+constexpr int kXMax = 113 * 1024;
+// What streams; the rest goes to the tensor memory GEMM.  Here and there, us:
+// eight tokens x 6144 x 6144 11.1, 12.3; x 12288 x 6144 13.9, 19.7; x 1024 x 1024
+// 2.5, 3.6; nine x 2048 x 2048 4.4, 4.0; 12 x 12288 x 2048 9.1, 8.4.  With few
+// rows the rounding of x, which every CTA does, weighs more than the products,
+// and the GEMM shares the columns out: eight x 512 x 6144 7.4, 4.9; seven x 2048 x
+// 4096 5.4, 5.1; six x 2048 x 4096 4.9, 5.0.
+constexpr int kStreamTok = 8;
+constexpr int kStreamRounding = 28000;
 
 struct StreamPlan {
     int wk_log, wr_log;  // warps along the columns, teams: 1 << each
@@ -37,7 +43,7 @@ __host__ __device__ constexpr int red_floats(int ntok) {
 }
 
 template <int NW, int NT, bool kCoarse>
-__global__ void __launch_bounds__(32 * NW, NW == 8 ? 3 : 1) linear_stream_kernel(LinearArgs a, StreamPlan p) {
+__global__ void __launch_bounds__(32 * NW, NW == 8 ? (NT == 1 ? 3 : 2) : 1) linear_stream_kernel(LinearArgs a, StreamPlan p) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wk = 1 << p.wk_log, team = warp >> p.wk_log, j = warp & (wk - 1);
@@ -198,9 +204,8 @@ cudaError_t launch_stream(const LinearArgs& a, StreamPlan p, cudaStream_t stream
         if (e != cudaSuccess) return e;
         set[dev] = 1;
     }
-    const int per_sm = NW == 8 ? 3 : 1;
     p.tiles = (a.N + (16 << p.wr_log) - 1) >> (4 + p.wr_log);
-    const int grid = p.tiles < per_sm * sms() ? p.tiles : per_sm * sms();
+    const int grid = p.tiles < sms() ? p.tiles : sms();
     return launch_pdl(k, dim3(grid), dim3(32 * NW), smem, stream, a, p);
 }
 
@@ -209,9 +214,9 @@ cudaError_t launch_stream(const LinearArgs& a, const StreamPlan& p, cudaStream_t
     return a.gshift >= 7 ? launch_stream<NW, NT, true>(a, p, stream) : launch_stream<NW, NT, false>(a, p, stream);
 }
 
-int stream_tokens(const LinearArgs& a) {
-    const int fit = kXMax / (2 * x_stride<true>((a.K + kChunkK - 1) / kChunkK));
-    return fit < kStreamTok ? fit : kStreamTok;
+bool streams(const LinearArgs& a) {
+    if (a.T > kStreamTok || a.T * 2 * x_stride<true>((a.K + kChunkK - 1) / kChunkK) > kXMax) return false;
+    return a.T <= 4 || a.N > 16 * sms() || a.T * a.K <= kStreamRounding;
 }
 
 }  // namespace
@@ -219,7 +224,7 @@ int stream_tokens(const LinearArgs& a) {
 int linear_launches(const LinearArgs&) { return 1; }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
-    if (a.T > stream_tokens(a)) return launch_linear_gemm(a, stream);
+    if (!streams(a)) return launch_linear_gemm(a, stream);
     StreamPlan p = {};
     p.chunks = (a.K + kChunkK - 1) / kChunkK;
     while (p.wk_log < 3 && (1 << p.wk_log) < p.chunks) ++p.wk_log;
@@ -227,16 +232,19 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
         p.wr_log = (warps == 8 ? 3 : 4) - p.wk_log;
         return p;
     };
-    // Up to four tokens and 16 rows an SM: eight warps a CTA, the finest tiles,
-    // and room for the next launch to start beside it (1024 x 1024, one token 2.0
-    // us against 2.2 with 16 warps, four 2.2 and 2.5; one x 512 x 6144 3.2 and
-    // 3.7).  Otherwise 16 warps share the rounding of x (4096 x 6144: 5.1 us against
-    // 5.8; two tokens x 6144 x 6144 6.8 and 8.5; four tokens x 12288 x 6144 13.8,
-    // and 14.3 with 24 warps, which leave 80 registers a thread).
-    if (a.T <= 4 && a.N <= 16 * sms() && 3 * stream_smem<8, 1>(a) <= kSmemMax - 3 * 1024)
-        return launch_stream<8, 1>(a, teams(8), stream);
-    if (a.T <= 4) return launch_stream<16, 1>(a, teams(16), stream);
-    return a.T <= 8 ? launch_stream<16, 2>(a, teams(16), stream) : launch_stream<16, 4>(a, teams(16), stream);
+    // 16 rows an SM: eight warps a CTA, the finest tiles, and room for the next
+    // launch to start beside it (1024 x 1024, one token 2.0 us against 2.2 with 16
+    // warps, four 2.2 and 2.5, eight 2.5 and 3.1; one x 512 x 6144 3.2 and 3.7).
+    // Otherwise 16 warps share the rounding of x (4096 x 6144: 5.1 us against 5.8;
+    // two tokens x 6144 x 6144 6.8 and 8.5; four tokens x 12288 x 6144 13.8, and
+    // 14.3 with 24 warps, which leave 80 registers a thread).
+    const bool few_rows = a.N <= 16 * sms();
+    if (a.T <= 4) {
+        if (few_rows && 3 * stream_smem<8, 1>(a) <= kSmemMax - 3 * 1024) return launch_stream<8, 1>(a, teams(8), stream);
+        return launch_stream<16, 1>(a, teams(16), stream);
+    }
+    if (few_rows && 2 * stream_smem<8, 2>(a) <= kSmemMax - 2 * 1024) return launch_stream<8, 2>(a, teams(8), stream);
+    return launch_stream<16, 2>(a, teams(16), stream);
 }
 
 }  // namespace moe

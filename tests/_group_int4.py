@@ -47,25 +47,29 @@ def block_max(x, n):
     return p.amax(-1, keepdim=True).expand_as(p).reshape(T, -1)[:, :K]
 
 
+def streams(T, N, half):
+    """Whether a projection of these sizes surely runs on the weight-streaming kernel (148 SMs)."""
+    K = 2 * half
+    return T <= 8 and T * 2 * (K + 320) <= 113 * 1024 and (T <= 4 or N > 16 * 148 or T * K <= 28000)
+
+
 def linear_bound(x, w, s, group, add=None):
-    """How far an f32 result may be from linear64, element by element.  The weight-streaming kernel (up to 16 tokens)
-    holds an activation to within 2^-15 of the largest of its 256-column block; the tensor-core kernel (more tokens,
-    or activations past 96 KB of shared memory) rounds code * scale to bf16, half a step of which
-    is 2^-8 of the weight, from a scale held to 2^-16.  Sums: every product or group sum enters one f32 addition
+    """How far an f32 result may be from linear64, element by element.  The weight-streaming kernel (streams)
+    holds an activation to within 2^-15 of the largest of its 256-column block; the tensor-core kernel rounds
+    code * scale to bf16, half a step of which is 2^-8 of the weight, from a scale held to 2^-16.  Sums: every product or group sum enters one f32 addition
     chain no longer than K / 16 + 64 (2^-24 of the running magnitude each, doubled for the tensor cores' truncation)."""
     W = weights64(w, s, group).abs()
     mag = x.double().abs() @ W.t()
-    stream = x.shape[0] <= 16 and x.shape[0] * 2 * (x.shape[1] + 320) <= 96 * 1024
-    b = 2.0 ** -15 * (block_max(x, 256) @ W.t()) if stream else (2.0 ** -8 + 2.0 ** -16) * mag
+    b = 2.0 ** -15 * (block_max(x, 256) @ W.t()) if streams(x.shape[0], *w.shape) else (2.0 ** -8 + 2.0 ** -16) * mag
     b = b + (x.shape[1] / 16 + 64) * 2.0 ** -23 * mag
     return b if add is None else b + 2.0 ** -23 * (mag + add.double().abs())
 
 
-def linear_rms(T):
+def linear_rms(T, N, half):
     """Bound of the relative L2 error of an f32 result: activations to 2^-15 of a block's largest value (under 2^-13 of
     its r.m.s.), or weights rounded to bf16 (uniform within half a step of at most 2^-8: r.m.s. 2^-8 / sqrt(3) < 2^-8.7,
     independent errors)."""
-    return 2.0 ** -12 if T <= 16 else 2.0 ** -8.7
+    return 2.0 ** -12 if streams(T, N, half) else 2.0 ** -8.7
 
 
 def make_layer(shape, group, stype="f32", seed=0, device="cuda"):
