@@ -1,17 +1,17 @@
 // A whole MoE layer for a few tokens, with group-scaled int4 weights, in two
-// kernels (three when the router weights are large):
+// kernels (three when the router or the gate and up weights are large):
 //
 //   few_gate_up_kernel  router logits, selection, and h = silu(g) * u of every
 //                       touched expert and of the shared one
 //   few_down_kernel     the down projections, their weighted sum, the residual
 //
-// Both read each touched expert's weights once for all its tokens (group_stream.cuh)
-// and let the columns of an mma tile be the tokens themselves: token t is
+// Both read each touched expert's weights once for all its tokens
+// (group_stream.cuh) and let the columns of an mma tile be the tokens themselves: token t is
 // column pair t % 4 of every expert's product, so the down kernel adds all
 // experts of a row up in registers.  Of tokens q and q + 4 the one that picked
 // the expert takes the column; a second pass over a weight tile is needed only
 // where both did (lane_token; 64 experts of 2560 x 512, 8 of them picked, 8
-// tokens: LATER us, LATER with a pass for each touched half of the tokens).  A
+// tokens: 47.3 us, 49.7 with a pass for each touched half of the tokens).  A
 // column without a token is computed and not used.
 //
 // h is stored as the down kernel's int8 operands: per 32 columns two int8
@@ -23,8 +23,8 @@
 // kernels are held by their instructions (59 and 67 % of the issue slots at
 // five tokens, 49 and 33 % of DRAM's peak): about 300 a warp for 16 rows x 256
 // columns of the down kernel, of whose time the mma products take 14 % and the
-// loads of h 7 %.  64 experts of 1024 x 512, 2 picked, one token: 10.0 us against 0.95,
-// none of it bandwidth: the chain logits - exchange - selection (1.0) - first
+// loads of h 7 %.  64 experts of 1024 x 512, 2 picked, one token: 10.0 us against
+// 0.95, none of it bandwidth: the chain logits - exchange - selection (1.0) - first
 // routed weights from HBM (1.4) - down (2.4), and two launches.
 #include <cooperative_groups.h>
 
