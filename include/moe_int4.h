@@ -162,7 +162,9 @@ typedef struct moe_shared_weights {
  *                    least one), re-weighted as routed_scaling * s /
  *                    (sum of the kept s); the dropped picks are not computed
  *                    and appear in topk_idx_out as -1 (weight 0) after the
- *                    kept ones.  The keep decision is taken in f32. */
+ *                    kept ones.  The keep decision is taken in f32; where
+ *                    the K's total is NaN every pick is kept, with a NaN
+ *                    weight. */
 typedef struct moe_cfg {
     uint32_t struct_size;
     int32_t H, E, K, I, Is;

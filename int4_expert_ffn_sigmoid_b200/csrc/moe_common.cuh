@@ -65,7 +65,9 @@ constexpr unsigned kFlagWeightsInt8 = 1u << 11;  // MOE_WEIGHTS_INT8
 // Adaptive expert top-p over the K picks of one token (one warp; lanes k < K
 // hold pick k: expert e_k and sigmoid score s_k; ssum is the K scores' sum).
 // A pick is kept when the scores of the picks ordered before it (score
-// descending, ties to the lower expert index) sum to less than p * ssum.
+// descending, ties to the lower expert index) sum to less than p * ssum; the
+// first one always (p * ssum is 0 where every score underflows), and all of
+// them where ssum is NaN, as without top-p: the weights are NaN then.
 // Returns on lane o < K the o-th kept pick (in pick order) with weight
 // scale * s / (sum of the kept s, added in pick order), and e = -1, w = 0 past
 // the kept ones.  p outside (0, 1): every pick, with weight scale * s / ssum.
@@ -77,12 +79,16 @@ __device__ __forceinline__ void topp_picks(int K, float p, float scale, int lane
         return;
     }
     float before = 0.f;
+    bool first = true;
     for (int j = 0; j < K; ++j) {
         const float sj = __shfl_sync(0xffffffffu, my_s, j);
         const int ej = __shfl_sync(0xffffffffu, my_e, j);
-        if (j != lane && (sj > my_s || (sj == my_s && ej < my_e))) before += sj;
+        if (j != lane && (sj > my_s || (sj == my_s && ej < my_e))) {
+            before += sj;
+            first = false;
+        }
     }
-    const unsigned km = __ballot_sync(0xffffffffu, lane < K && before < p * ssum);
+    const unsigned km = __ballot_sync(0xffffffffu, lane < K && (first || !(before >= p * ssum)));
     float kept = 0.f;
     out_e = -1;
     out_w = 0.f;

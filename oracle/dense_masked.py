@@ -50,12 +50,12 @@ def topp_keep(s_sel: np.ndarray, e_sel: np.ndarray, p: float) -> np.ndarray:
     highest-scoring ones (ties: lower expert index) whose scores reach p of the
     K picks' total.  Written as a search over prefix lengths: the smallest n
     such that the n best picks carry at least p of the total (a pick is needed
-    while the mass before it is still below p)."""
+    while the mass before it is still below p), at least one."""
     order = sorted(range(len(s_sel)), key=lambda k: (-s_sel[k], e_sel[k]))
     total = float(np.sum(s_sel))
     keep = np.zeros(len(s_sel), bool)
     for n in range(1, len(order) + 1):
-        if sum(s_sel[order[j]] for j in range(n - 1)) >= p * total:
+        if n > 1 and sum(s_sel[order[j]] for j in range(n - 1)) >= p * total:
             break
         keep[order[n - 1]] = True
     return keep

@@ -134,7 +134,7 @@ static void apply_topp(double topp, double scale, const double* scores, int K, i
     for (int j = 0; j < K; ++j) {
         double d = fabs(cum - topp * total) / total;
         if (d < mm) mm = d;
-        if (cum < topp * total) {
+        if (j == 0 || !(cum >= topp * total)) { /* at least one; all of them for a NaN total */
             keep[ord[j]] = 1;
             cum += scores[idx[ord[j]]];
         }
