@@ -234,10 +234,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_gate_up_kernel(FewArgs a) 
     if (size > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started
     if (tid < a.E) s_bias[tid] = __ldg(a.rb + tid);
     if (tid < kMaxE / 32) s_mask[tid] = 0;
-    // expert 0 for the unused ones: whatever mix of two calls' picks a shared
-    // workspace came to hold would still be experts
+    // Unused entries name expert 0 and slot 0: of a workspace that two calls use
+    // at once (which is not allowed) the down kernel may read a mix of their
+    // tables, and sums that are wrong are better than addresses out of range.
     if (tid < kFewMaxU) P.tokens[tid] = 0, P.expert[tid] = 0;
-    if (tid < kFewMaxU * kFewTok) P.slot[tid / kFewTok][tid % kFewTok] = -1;
+    if (tid < kFewMaxU * kFewTok) P.slot[tid / kFewTok][tid % kFewTok] = 0;
     static_assert(kFewCluster <= 8, "a lane of eight per CTA");
     static_assert(kFewThreads >= kFewMaxU * kFewTok, "one slot a thread");
     // The dot products of this CTA's experts.  Of eight experts and fewer, with
@@ -554,14 +555,15 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
         Unit d;
         const bool sh = v < Cs;
         const int u = sh ? -1 : (v - Cs) / Ci, c = sh ? v : v - Cs - u * Ci;
-        const size_t row = sh ? 0 : (size_t)P.expert[u] * a.H;
+        // in range whatever the table holds (see few_gate_up_kernel)
+        const size_t row = sh ? 0 : (size_t)min((unsigned)P.expert[u], (unsigned)a.E - 1) * a.H;
         d.I = (int16_t)(sh ? a.Is : a.I);
         d.G = (int16_t)(sh ? a.Gs2 : a.G2);
         d.w = (sh ? a.sh_w2 : a.w2) + row * (d.I / 2) + c * (kChunkK / 2);
         d.s = static_cast<const char*>(sh ? a.sh_s2 : a.s2) + ((row * d.G) << (a.stype == kScaleF32 ? 2 : 1));
         d.u = (int16_t)u;
         d.c = (uint8_t)c;
-        d.tokens = (uint8_t)(sh ? (1u << T) - 1 : P.tokens[u]);
+        d.tokens = (uint8_t)(sh ? (1u << T) - 1 : max(P.tokens[u], 1u));
         return d;
     };
     for (int v = tid; v < Cs; v += kDownThreads) list[v] = describe(v);
@@ -608,7 +610,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) few_down_kernel(FewArgs a) {
     for (int i = tid; i < (int)(sizeof(FewPicks) / 4); i += kDownThreads)
         reinterpret_cast<int*>(&P)[i] = __ldcg(reinterpret_cast<const int*>(a.picks) + i);
     __syncthreads();
-    units = Cs + min(P.U, T * a.K) * Ci;
+    units = Cs + max(min(P.U, min(a.E, T * a.K)), 0) * Ci;
     for (int v = Cs + tid; v < units; v += kDownThreads) list[v] = describe(v);
     __syncthreads();
     all = true;

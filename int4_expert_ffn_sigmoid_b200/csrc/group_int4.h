@@ -34,7 +34,7 @@ struct FewPicks {
     int U;                           // touched experts
     int expert[kFewMaxU];            // ascending
     unsigned tokens[kFewMaxU];       // bit t: token t picked it
-    int8_t slot[kFewMaxU][kFewTok];  // t * K + k of token t's pick of the expert, or -1
+    int8_t slot[kFewMaxU][kFewTok];  // t * K + k of token t's pick of the expert (0 where it has none)
 };
 
 struct FewArgs {

@@ -316,3 +316,25 @@ def test_tokens_that_share_a_column(moe, cuda_device, stype, group):
         out = check(moe, y, L, shape, group)
         for t, s in enumerate(other):  # equal tokens, equal rows
             assert torch.equal(out[t], out[other.index(s)])
+
+
+@pytest.mark.parametrize("T", [1, 3, 8])
+def test_every_word_of_the_picks_table_is_in_range(moe, cuda_device, T):
+    """The table at the workspace's start (count, experts, token masks, slots): unused entries too name an expert and a
+    slot, so that no mix of two tables leads out of the weights or the workspace."""
+    shape = shape_of(256, 12, 3, 128, 128)
+    L = make_layer(shape, 64, "bf16", device=cuda_device)
+    m = moe.MoEFewLayer(L, shape, 64)
+    x = tokens(T, shape, L, 71, cuda_device)
+    idx = torch.empty((T, 3), dtype=torch.int32, device=cuda_device)
+    m(x, topk_idx=idx)
+    table = m.workspace[:4 * 257].cpu()
+    words, slots = table.view(torch.int32), table[4 * 129:].view(torch.int8).view(64, 8)
+    used = sorted(set(idx.flatten().tolist()))
+    assert int(words[0]) == len(used) and words[1:1 + len(used)].tolist() == used
+    assert bool(((words[1:65] >= 0) & (words[1:65] < 12)).all())
+    assert bool((slots >= 0).all() and (slots < T * 3).all())
+    for t in range(T):
+        for k, e in enumerate(idx[t].tolist()):
+            u = used.index(e)
+            assert int(slots[u, t]) == t * 3 + k and (int(words[65 + u]) >> t) & 1
