@@ -496,8 +496,9 @@ int32_t moe_few_kernel_launches(const moe_few_cfg_t* cfg, int32_t T);
  * multiplied in, is rounded in the same way over 32 columns each.  The router
  * is f32 throughout.  A workspace serves one call at a time: streams, and
  * captured graphs that may run at the same time, have one each.
- * x: bf16 [T][H]; out: bf16 [T][H] (f32 under MOE_OUT_F32), not overlapping x;
- * T: 0..2^20.  More than moe_few_pass_tokens(cfg) tokens run in passes of that
+ * x: bf16 [T][H]; out: bf16 [T][H] (f32 under MOE_OUT_F32); T: 0..2^20.  out,
+ * the workspace and the pick outputs overlap neither each other nor what the
+ * call reads.  More than moe_few_pass_tokens(cfg) tokens run in passes of that
  * many, each reading its experts' weights again: any T is served, and a call
  * for many tokens belongs to moe_layer_forward (per-row scales). */
 int moe_few_forward(const void* x, const moe_few_weights_t* w, void* out, int32_t T, const moe_few_cfg_t* cfg,

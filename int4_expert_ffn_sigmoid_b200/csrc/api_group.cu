@@ -36,7 +36,7 @@ size_t scale_bytes(int stype) { return stype == kScaleF32 ? 4 : 2; }
 
 struct Range {
     uintptr_t lo, hi;
-    bool meets(const Range& o) const { return lo < o.hi && o.lo < hi; }
+    bool meets(const Range& o) const { return lo < o.hi && o.lo < hi && lo < hi && o.lo < o.hi; }
 };
 Range range(const void* p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + bytes}; }
 
@@ -163,11 +163,26 @@ int moe_few_forward(const void* x, const moe_few_weights_t* w, void* out, int32_
         if (a.Is > 0 && (!p || !aligned(p, 16))) return MOE_ERR_INVALID_ARG;
     if (!aligned(cfg->topk_idx_out, 16) || !aligned(cfg->topk_w_out, 16)) return MOE_ERR_INVALID_ARG;
     const size_t osz = (a.flags & MOE_OUT_F32) ? 4 : 2, n = (size_t)T * a.H;
-    if (range(out, n * osz).meets(range(x, n * 2))) return MOE_ERR_INVALID_ARG;
     const size_t need_ws = moe_few_workspace_bytes(cfg, T);
     if (!cfg->workspace || cfg->workspace_bytes < need_ws) return MOE_ERR_WORKSPACE;
     if (!aligned(cfg->workspace, 256)) return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
+    // What a call writes meets nothing else that it reads or writes.
+    const size_t tk = (size_t)T * a.K, sb = scale_bytes(a.stype), E = a.E, H = a.H, I = a.I, Is = a.Is;
+    const Range writes[] = {range(out, n * osz), range(cfg->workspace, need_ws),
+                            range(cfg->topk_idx_out, cfg->topk_idx_out ? tk * 4 : 0),
+                            range(cfg->topk_w_out, cfg->topk_w_out ? tk * 4 : 0)};
+    const Range reads[] = {range(x, n * 2), range(w->router_w, E * H * 4), range(w->router_bias, E * 4),
+                           range(w->w13, E * I * H), range(w->s13, E * 2 * I * a.G13 * sb),
+                           range(w->w2, E * H * I / 2), range(w->s2, E * H * a.G2 * sb),
+                           range(w->sh_w13, Is * H), range(w->sh_s13, 2 * Is * a.G13 * sb),
+                           range(w->sh_w2, H * Is / 2), range(w->sh_s2, H * a.Gs2 * sb)};
+    for (const Range& o : writes) {
+        for (const Range& r : reads)
+            if (o.meets(r)) return MOE_ERR_INVALID_ARG;
+        for (const Range& r : writes)
+            if (&o != &r && o.meets(r)) return MOE_ERR_INVALID_ARG;
+    }
     a.rw = w->router_w;
     a.rb = w->router_bias;
     a.w13 = w->w13;

@@ -129,3 +129,36 @@ def test_binding_refuses_host_tensors(moe):
         moe.Int4Linear(torch.zeros((4, 16), dtype=torch.uint8), torch.zeros((4, 1)), 32)
     with pytest.raises(ValueError):
         moe.Int4Linear(torch.zeros(16, dtype=torch.uint8), torch.zeros((4, 1)), 32)
+
+
+def test_few_refuses_overlaps(moe):
+    """out, the workspace and the pick outputs meet nothing else that the call reads or writes."""
+    INV = moe.MOE_ERR_INVALID_ARG
+    shape = shape_of(256, 8, 2, 128, 128)
+    reads = [n for n, _ in moe.moe_few_weights_t._fields_]
+    at = {n: (20 + i) << 20 for i, n in enumerate(reads)}  # every tensor a MB of its own
+
+    def call(out=0, ws=1 << 20, idx=2 << 20, w=3 << 20, x=4 << 20, flags=0, T=8):
+        def spread(p):
+            for n, a in at.items():
+                setattr(p, n, a)
+
+        def picks(c):
+            c.topk_idx_out, c.topk_w_out = idx, w
+        return few(moe, shape, T, out=out, ws=ws, x=x, flags=flags, patch=picks, wpatch=spread)
+
+    ws_bytes = moe.few_workspace_bytes(shape, 8, 32)
+    sizes = {"router_w": 8 * 256 * 4, "router_bias": 8 * 4, "w13": 8 * 256 * 128, "s13": 8 * 256 * 8 * 4,
+             "w2": 8 * 256 * 64, "s2": 8 * 256 * 4 * 4, "sh_w13": 256 * 128, "sh_s13": 256 * 8 * 4, "sh_w2": 256 * 64,
+             "sh_s2": 256 * 4 * 4}
+    assert set(sizes) == set(reads)
+    for n, size in sizes.items():
+        first, last = at[n], at[n] + size - 16
+        assert call(out=first) == INV and call(out=last) == INV and call(out=first - 16) == INV, n
+        assert call(out=1 << 20, ws=first) == INV, n
+        assert call(out=64 << 20, idx=first) == INV and call(out=64 << 20, w=last) == INV, n
+    out = 64 << 20
+    assert call(out=out, ws=out) == INV and call(out=out, ws=out - ws_bytes // 256 * 256 + 256) == INV
+    assert call(out=out, idx=out + 8 * 256 * 2 - 16) == INV and call(out=out, flags=moe.MOE_OUT_F32, w=out + 8 * 256 * 2) == INV
+    assert call(out=out, idx=3 << 20, w=3 << 20) == INV and call(out=out, ws=4 << 20) == INV and call(out=out, idx=4 << 20) == INV
+    assert call(out=4 << 20, T=0) == 0  # nothing is read or written
