@@ -772,17 +772,27 @@ bool get_encode() {
     return true;
 }
 
+// The driver's encoder.  It needs a current context, which a host thread that
+// has launched nothing yet does not have, whatever the others did: binding the
+// device gives it one.
+bool encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box, CUtensorMapSwizzle sw) {
+    const cuuint32_t es[2] = {1, 1};
+    auto call = [&] {
+        return g_encode(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    int dev = 0;
+    return call() || (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && call());
+}
+
 // 2-D tensor map over a row-major [rows][inner] matrix.
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, uint64_t inner, uint64_t rows,
               uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw) {
     cuuint64_t dims[2] = {inner, rows};
     cuuint64_t strides[1] = {inner * (uint64_t)esize};
     cuuint32_t box[2] = {box_inner, box_rows};
-    cuuint32_t es[2] = {1, 1};
-    const CUresult r = g_encode(m, dt, 2, const_cast<void*>(base), dims, strides, box, es,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode(m, dt, base, dims, strides, box, sw);
 }
 
 int g_smem_set[64];
@@ -810,9 +820,7 @@ bool encode_tensor_map_rows(CUtensorMap* m, CUtensorMapDataType dt, const void* 
     cuuint64_t dims[2] = {inner, rows};
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {box_inner, box_rows};
-    cuuint32_t es[2] = {1, 1};
-    return g_encode(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, dt, base, dims, strides, box, sw);
 }
 
 int tc_smem_bytes() { return tc::smem_bytes<4>(); }
