@@ -139,7 +139,7 @@ int validate_cfg(const moe_cfg_t* c) {
 inline bool aligned(const void* ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }
 
 int sm_count() {
-    static int cache[64];
+    static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
     if (dev < 0 || dev >= 64) dev = 0;

@@ -1319,7 +1319,7 @@ int fused_rows2(int H, int E, int K, int I, int Is, int T, int sms) {
 }
 
 cudaError_t launch_decode_stack(const FArgs& a, int grid, cudaStream_t stream) {
-    static int attr_set[64];
+    static std::atomic<int> attr_set[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
     if (!attr_set[dev]) {
@@ -1357,7 +1357,7 @@ cudaError_t launch_decode_stack(const FArgs& a, int grid, cudaStream_t stream) {
 }
 
 int fused_grid() {
-    static int cache[64];
+    static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
     if (cache[dev] == 0) {

@@ -2082,11 +2082,11 @@ bool w13_tma(int H) { return H >= kTmaMinH && H % kTmaChunk == 0; }
 
 template <typename Kern>
 int resident(Kern kern, size_t smem, int which, int threads = 256) {
-    static int cache[16][64];  // by kernel (`which`) and device
+    static std::atomic<int> cache[16][64];  // by kernel (`which`) and device
     static_assert(kSmem13Bulk <= 227 * 1024, "bulk gate/up shared memory");
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-    int& c = cache[which][dev];
+    std::atomic<int>& c = cache[which][dev];
     if (c == 0) {
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         int per_sm = 0, sms = 0;

@@ -759,7 +759,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmX_r, const __grid_cons
 
 namespace {
 
-PFN_encodeTiled g_encode = nullptr;
+std::atomic<PFN_encodeTiled> g_encode{nullptr};
 
 bool get_encode() {
     if (g_encode) return true;
@@ -779,7 +779,7 @@ bool encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const cuui
             const cuuint32_t* box, CUtensorMapSwizzle sw) {
     const cuuint32_t es[2] = {1, 1};
     auto call = [&] {
-        return g_encode(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+        return g_encode.load()(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     int dev = 0;
@@ -795,7 +795,7 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* bas
     return encode(m, dt, base, dims, strides, box, sw);
 }
 
-int g_smem_set[64];
+std::atomic<int> g_smem_set[64];
 
 template <int WB>
 cudaError_t set_smem_attrs() {

@@ -717,7 +717,7 @@ namespace {
 // SMs of the current device, and the CTAs of the gate/up kernel that run at
 // once in clusters of kFewCluster.
 struct FewDevice {
-    int sms, clustered;
+    std::atomic<int> sms, clustered;  // clustered = 0: not asked yet; written last
 };
 
 cudaError_t few_launch_cluster(void (*k)(FewArgs), int grid, int cluster, size_t smem, cudaStream_t stream, const FewArgs& a,
@@ -765,7 +765,8 @@ cudaError_t few_launch(const FewArgs& a, cudaStream_t stream) {
         d.clustered = n * kFewCluster;
     }
     const size_t smem = few_smem(NT, a.T, a.H, x_stride<kCoarse>((a.H + kChunkK - 1) / kChunkK), a.lslices > 0);
-    const int cluster = a.lslices > 0 ? 1 : kFewCluster, most = a.lslices > 0 ? d.sms : d.clustered;
+    const int sms = d.sms, clustered = d.clustered;
+    const int cluster = a.lslices > 0 ? 1 : kFewCluster, most = a.lslices > 0 ? sms : clustered;
     const int tiles = few_tiles(a);
     int grid = (tiles + cluster - 1) / cluster * cluster;
     if (grid > most) grid = most;
@@ -775,7 +776,7 @@ cudaError_t few_launch(const FewArgs& a, cudaStream_t stream) {
     const size_t smem_down = (size_t)kDownWarps * kDownDepth * kStageBytes + 2 * (size_t)kDownWarps * 4 * NT * 16 * 4 +
                              units * sizeof(Unit);
     if (e == cudaSuccess)
-        e = launch_pdl(down, dim3(out_tiles < d.sms ? out_tiles : d.sms), dim3(kDownThreads),
+        e = launch_pdl(down, dim3(out_tiles < sms ? out_tiles : sms), dim3(kDownThreads),
                        smem_down, stream, a);
     return e;
 }

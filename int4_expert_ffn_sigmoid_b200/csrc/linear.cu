@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 8 ? (NT == 1 ? 3 : 2) : 1) line
 namespace {
 
 int sms() {
-    static int cache[64];
+    static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
     if (cache[dev] == 0) {
@@ -197,7 +197,7 @@ template <int NW, int NT, bool kCoarse>
 cudaError_t launch_stream(const LinearArgs& a, StreamPlan p, cudaStream_t stream) {
     const size_t smem = stream_smem<NW, NT>(a);
     auto* k = linear_stream_kernel<NW, NT, kCoarse>;
-    static int set[64];
+    static std::atomic<int> set[64];
     int dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && !set[dev]) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);

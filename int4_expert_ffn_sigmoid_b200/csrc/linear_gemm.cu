@@ -484,11 +484,12 @@ template <int kN, bool kLow>
 cudaError_t launch(const LinearArgs& a, int dev, int size, cudaStream_t stream) {
     auto* k = linear_gemm_kernel<kN, kLow>;
     using G = Geo<kN>;
-    static int set[64];
-    cudaError_t e = cudaSuccess;
-    if (!set[dev]) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
-    if (e != cudaSuccess) return e;
-    set[dev] = 1;
+    static std::atomic<int> set[64];
+    if (!set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+        if (e != cudaSuccess) return e;
+        set[dev] = 1;
+    }
     GemmPlan p;
     p.stages = (a.K + kStageK - 1) / kStageK;
     p.row_tiles = (a.N + kRows - 1) / kRows;
@@ -516,7 +517,7 @@ cudaError_t launch(const LinearArgs& a, int dev, int size, cudaStream_t stream) 
 
 // CTAs of a cluster size that run at once, of any of the kernels (one an SM).
 struct Capacity {
-    int ctas[9];  // [1] = 0: not asked yet
+    std::atomic<int> ctas[9];  // [1] = 0: not asked yet; written last
 };
 cudaError_t capacity(int dev, const Capacity** out) {
     static Capacity caps[64];

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>  // host side: facts asked once per device, by whichever thread is first
+
 namespace moe {
 
 // Largest T that takes the weight-streaming (small-batch) path by default.

@@ -1018,7 +1018,7 @@ cudaError_t launch_router(const Params& p, bool small_path, cudaStream_t stream)
     cudaError_t err;
     if (small_path) {
         const size_t smem = router_decode_smem(p.H);
-        static int attr_set[64];
+        static std::atomic<int> attr_set[64];
         int dev = 0;
         if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && !attr_set[dev]) {
             const cudaError_t e = cudaFuncSetAttribute(router_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

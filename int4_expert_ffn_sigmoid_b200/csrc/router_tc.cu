@@ -354,7 +354,7 @@ namespace {
 template <int N>
 cudaError_t launch_n(const Params& p, const rtc::Geom& g, const CUtensorMap& mx, const CUtensorMap& mw,
                      cudaStream_t stream) {
-    static int attr_set[64];
+    static std::atomic<int> attr_set[64];
     int dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && !attr_set[dev]) {
         const cudaError_t e = cudaFuncSetAttribute(router_logits_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -1,4 +1,7 @@
 """Calls from several host threads."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -52,3 +55,42 @@ def test_first_call_of_a_thread(cuda_device):
         t.join()
         assert isinstance(got[0], torch.Tensor), (name, got[0])
         assert torch.equal(got[0], want), name
+
+
+def run_at_once(times=4):
+    """The calls, `times` each, every one from a thread and on a stream of its own, as a process's first launches."""
+    import int4_expert_ffn_sigmoid_b200 as moe
+    work = [c for _ in range(times) for c in calls(moe, torch.device("cuda:0"))]
+    streams = [torch.cuda.Stream() for _ in work]
+    got, start = [None] * len(work), threading.Barrier(len(work))
+    torch.cuda.synchronize()
+
+    def run(i):
+        start.wait()
+        try:
+            with torch.cuda.stream(streams[i]):
+                got[i] = work[i][1]()
+        except Exception as e:  # noqa: BLE001
+            got[i] = e
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for (name, call), o in zip(work, got):
+        assert isinstance(o, torch.Tensor), (name, o)
+        first = o.clone()
+        assert torch.equal(call(), first), name
+    print("ok", len(work))
+
+
+@pytest.mark.parametrize("again", range(3))
+def test_first_calls_of_a_process_at_once(cuda_device, again):
+    """What a launch asks once per device (SM count, cluster capacity, shared memory limits) reaches the other threads
+    whole, whichever is first."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", "from tests.test_gpu_threads import run_at_once; run_at_once()"], cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
