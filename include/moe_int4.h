@@ -104,6 +104,8 @@ extern "C" {
                                        MOE_FORCE_DECODE on them is MOE_ERR_UNSUPPORTED.  Expert bit
                                        width of the checkpoint converter: nanocolibri-engine
                                        README, "Converting a checkpoint yourself" */
+#define MOE_FULL_WEIGHTS (1u << 13) /* moe_linear_forward: more than eight tokens keep what the
+                                       rounding of a weight to bf16 leaves (see there) */
 
 /* Device status word: the first 4 bytes of the workspace hold the OR of these
  * bits after a call completes on the device (0 = no check failed).  Under
@@ -396,14 +398,20 @@ int32_t moe_layer_path(const moe_cfg_t* cfg, int32_t T);
  *
  * Arithmetic of both operators: f32 sums throughout, one rounding to bf16 at
  * the end (none under MOE_OUT_F32), the same bits for the same call every
- * time.  Weight streaming (up to eight tokens, fewer where rows are long and
- * few) multiplies the codes with x
+ * time.  Weight streaming (up to eight tokens whose activations fit in shared
+ * memory: T * (K rounded up to 256, + 64) to 57856) multiplies the codes with x
  * rounded to 16 bits, two int8 parts and a power-of-two scale: off by at most
  * 2^-15 of the largest magnitude of the 256 columns (k / 256) it is in, exact
  * integer sums within a scale group.  256 columns whose magnitudes are all
  * below 2^-113 count as zero; a token with a NaN or an infinity gets NaN in
- * every output.  More tokens run on the bf16 tensor cores: x as it is, each
- * weight c * scale rounded to bf16 once.
+ * every output.  The other calls of moe_linear_forward run on the bf16 tensor
+ * cores with x as it is.  Up to eight tokens, and with MOE_FULL_WEIGHTS any
+ * number, they take each weight c * scale in two bf16 parts, off by at most
+ * 2^-16 of it: one accuracy for one token and for eight.  More tokens take it
+ * in one part, rounded once to bf16 (off by up to 2^-8 of it): beside a bf16
+ * output's own rounding (relative L2 error 1.7e-3) the result is then off by
+ * 2.0e-3 to 2.4e-3, and under MOE_OUT_F32 by 1.2e-3 to 1.7e-3 where the full
+ * weights leave 2e-6 to 7e-6, for 1.2 to 1.7 times the time.
  * ------------------------------------------------------------------------- */
 #define MOE_SCALE_F32 0
 #define MOE_SCALE_BF16 1
@@ -415,7 +423,7 @@ int32_t moe_layer_path(const moe_cfg_t* cfg, int32_t T);
  *   K           : input features, a multiple of 32, 32..32768
  *   group       : columns per scale (see above)
  *   scale_type  : MOE_SCALE_*
- *   flags       : MOE_OUT_F32 (out is f32), or 0
+ *   flags       : MOE_OUT_F32 (out is f32), MOE_FULL_WEIGHTS (see above)
  *   ldx         : elements between rows of x (0: K); a multiple of 8, >= K
  *   ldo, lda    : elements between rows of out and of add (0: N), >= N */
 typedef struct moe_linear_cfg {

@@ -28,6 +28,7 @@ __all__ = [
     "workspace_bytes", "workspace_bytes_upto", "layer_forward", "MoELayer", "decode_max_tokens", "kernel_launches", "layer_path",
     "MOE_PATH_SMALL_BATCH", "MOE_PATH_TENSOR_CORE", "MOE_PATH_LARGE_STREAMING", "LIB_PATH",
     "moe_linear_cfg_t", "moe_few_cfg_t", "moe_few_weights_t", "MOE_SCALE_F32", "MOE_SCALE_BF16", "MOE_SCALE_F16",
+    "MOE_FULL_WEIGHTS",
     "linear_forward", "linear_kernel_launches", "Int4Linear",
     "few_forward", "few_workspace_bytes", "few_pass_tokens", "few_kernel_launches", "MoEFewLayer",
 ]
@@ -53,6 +54,7 @@ MOE_TRACE = 1 << 8
 MOE_DEBUG_POISON = 1 << 9
 MOE_STACK_FUSED = 1 << 10
 MOE_WEIGHTS_INT8 = 1 << 11
+MOE_FULL_WEIGHTS = 1 << 13
 TRACE_SLOTS = 16  # MOE_TRACE stamps per (CTA, layer)
 # device status word (the first 4 bytes of the workspace)
 MOE_DEVSTAT_BAD_EXPERT = 1 << 0
@@ -509,7 +511,8 @@ class Int4Linear:
     def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
                  flags: int = 0, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """out[t] = W x[t] (+ add[t]).  x: bfloat16 [T, K], add: bfloat16 [T, N], out: bfloat16 (float32 under
-        MOE_OUT_F32) [T, N]; each may have rows further apart than their length.  ``out`` may be ``add``."""
+        MOE_OUT_F32) [T, N]; each may have rows further apart than their length.  ``out`` may be ``add``.  Above eight
+        tokens the weights are rounded to bf16 unless ``flags`` holds MOE_FULL_WEIGHTS."""
         shape, cref, ap = x.shape, self._cref, None
         T = shape[0] if shape else -1
         # the common call, without a look at each tensor's strides

@@ -11,6 +11,9 @@ namespace moe {
 // Scale types (the MOE_SCALE_* values of the C ABI).
 constexpr int kScaleF32 = 0, kScaleBf16 = 1, kScaleF16 = 2;
 
+// Tokens of a projection that weight streaming takes at most.
+constexpr int kStreamTok = 8;
+
 // log2 of the columns per scale; kRowGroup: one scale a row (k >> kRowGroup
 // is 0 for every column).
 constexpr int kRowGroup = 31;
@@ -24,6 +27,7 @@ struct LinearArgs {
     int T, N, K;
     int gshift, G;  // columns per scale: 1 << gshift; scales per row
     int stype, out_f32;
+    int full;  // MOE_FULL_WEIGHTS
     long long ldx, ldo, lda;
 };
 

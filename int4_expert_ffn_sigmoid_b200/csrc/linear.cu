@@ -23,14 +23,6 @@ constexpr int kDepth = 3;
 // (eight tokens of 7168 columns).
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kXMax = 113 * 1024;
-// What streams; the rest goes to the tensor memory GEMM.  Here and there, us:
-// eight tokens x 6144 x 6144 11.1, 12.3; x 12288 x 6144 13.9, 19.7; x 1024 x 1024
-// 2.5, 3.6; nine x 2048 x 2048 4.4, 4.0; 12 x 12288 x 2048 9.1, 8.4.  With few
-// rows the rounding of x, which every CTA does, weighs more than the products,
-// and the GEMM shares the columns out: eight x 512 x 6144 7.4, 4.9; seven x 2048 x
-// 4096 5.4, 5.1; six x 2048 x 4096 4.9, 5.0.
-constexpr int kStreamTok = 8;
-constexpr int kStreamRounding = 28000;
 
 struct StreamPlan {
     int wk_log, wr_log;  // warps along the columns, teams: 1 << each
@@ -214,9 +206,14 @@ cudaError_t launch_stream(const LinearArgs& a, const StreamPlan& p, cudaStream_t
     return a.gshift >= 7 ? launch_stream<NW, NT, true>(a, p, stream) : launch_stream<NW, NT, false>(a, p, stream);
 }
 
+// Up to eight tokens stream where their activations fit; the rest goes to the
+// tensor memory GEMM.  Here and there, us: eight tokens x 6144 x 6144 11.1, 12.3;
+// x 12288 x 6144 13.9, 19.7; x 1024 x 1024 2.5, 3.6; nine x 2048 x 2048 4.4, 4.0;
+// 12 x 12288 x 2048 9.1, 8.4.  A GEMM as accurate for eight tokens (see
+// linear_gemm.cu) is no faster but for a few hundred rows: eight x 512 x 6144
+// 7.4, 6.4; x 1024 x 6144 7.4, 8.0; x 2048 x 6144 7.8, 9.6; five x 512 x 6144 6.1, 6.5.
 bool streams(const LinearArgs& a) {
-    if (a.T > kStreamTok || a.T * 2 * x_stride<true>((a.K + kChunkK - 1) / kChunkK) > kXMax) return false;
-    return a.T <= 4 || a.N > 16 * sms() || a.T * a.K <= kStreamRounding;
+    return a.T <= kStreamTok && a.T * 2 * x_stride<true>((a.K + kChunkK - 1) / kChunkK) <= kXMax;
 }
 
 }  // namespace

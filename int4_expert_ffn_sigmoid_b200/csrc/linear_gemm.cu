@@ -7,13 +7,18 @@
 // per stage, accumulated in tensor memory over all columns (of this CTA's
 // share).  A is built in tensor memory from the packed codes: the converter
 // warps turn a row's codes into bf16 and multiply them by the row's group
-// scale, rounding each weight once (2^-8 of it at most; the codes 0, 1, 2, 4
-// and 8 times a bf16 scale are exact).  x enters as it is, by TMA.  A second
-// MMA per step with what the rounding left (exact to 2^-16) was built first
-// and taken out: an MMA with A in tensor memory takes 69 cycles at 64 tokens
-// and 84 at 128, so it held the kernel to the MMAs' pace (23.5 against 19.1 us
-// for 64 tokens x 6144 x 6144, 40.3 against 30.0 for 512 x 4096 x 6144) while
-// the bf16 output's own rounding (1.66e-3) is over twice what it removed.
+// scale.  x enters as it is, by TMA.
+//
+// Two forms.  One part: each weight is rounded once to bf16 (2^-8 of it at
+// most; the codes 0, 1, 2, 4 and 8 times a bf16 scale are exact).  Two parts
+// (kRest): what that rounding left is a second bf16 matrix and each step takes
+// a second MMA, which holds a weight to 2^-16.  Two parts are taken for up to
+// eight tokens, where weight streaming is as good and a token's accuracy should
+// not hang on its company, and under MOE_FULL_WEIGHTS.  They cost 64 tokens x
+// 6144 x 6144 13.5 -> 19.7 us, 512 x 4096 x 6144 22.6 -> 38.7, 16 x 6144 x 2048 6.3
+// -> 10.6: the MMAs' pace.  One part is the default for more tokens because a
+// bf16 output rounds as much again (relative L2 error 1.66e-3; the weights'
+// rounding adds 1.2e-3 with bf16 scales to 1.7e-3 with f32 ones).
 //
 // Few row tiles: a cluster of up to eight CTAs shares a tile's columns; each
 // leaves its part in shared memory and sums all parts of the chunks of eight
@@ -42,22 +47,23 @@ namespace {
 constexpr int kRows = 128, kStageK = 128;
 constexpr int kConvWarps = 24, kThreads = 32 * (kConvWarps + 3);
 constexpr int kWarpW = kConvWarps, kWarpX = kConvWarps + 1, kWarpMma = kConvWarps + 2;
-constexpr int kACols = 64;  // tensor memory columns of an A stage
 constexpr int kTmemCols = 512;
 constexpr int kWBytes = kRows * kStageK / 2;
 constexpr long long kWait = kBulkWaitCycles;
 
-template <int kN>
+// kRest: a second A matrix with what the rounding of the weights left.
+template <int kN, bool kRest>
 struct Geo {
+    static constexpr int kACols = kRest ? 128 : 64;  // tensor memory columns of an A stage
     // Stages of x and of A go together: the one commit after a stage's MMAs
     // frees both.  The codes have a deeper ring of their own.
     static constexpr int kXBytes = kN * kStageK * 2;
-    static constexpr int kStages = kN == 256 ? 3 : kN == 128 ? 4 : 6;
+    static constexpr int kStages = kRest || kN == 256 ? 3 : kN == 128 ? 4 : 6;
     static constexpr int kWStages = kN == 256 ? 3 : 6;
     // Converter warps: kGroups take the stages in turn; of a stage's two
     // 64-column halves a warp takes both (kSplit = 1: less to do per stage, and
     // more stages under way) or one (2: where shared memory holds few stages).
-    static constexpr int kSplit = kN >= 128 ? 2 : 1;
+    static constexpr int kSplit = kRest || kN >= 128 ? 2 : 1;
     static constexpr int kGroups = kConvWarps / (4 * kSplit);
     // A barrier's phase is told apart by its parity alone, so nobody may wait
     // for a phase before the one ahead of it is over.  A slot of the code ring
@@ -115,6 +121,13 @@ __device__ __forceinline__ void st_tmem32(uint32_t at, const uint32_t (&o)[32]) 
         "r"(o[28]), "r"(o[29]), "r"(o[30]), "r"(o[31])
         : "memory");
 }
+__device__ __forceinline__ void st_tmem16(uint32_t at, const uint32_t (&o)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(at),
+        "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(o[8]), "r"(o[9]),
+        "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
+        : "memory");
+}
 __device__ __forceinline__ void ld_tmem8(uint32_t at, float (&v)[8]) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;\n"
@@ -136,7 +149,9 @@ __device__ __forceinline__ ScaleParts split_scale(uint32_t raw, int stype) {
         const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&two);
         return {s, s};
     }
-    const float s = stype == kScaleF32 ? __uint_as_float(raw) : __half2float(__ushort_as_half((unsigned short)raw));
+    const float s = stype == kScaleF32    ? __uint_as_float(raw)
+                    : stype == kScaleBf16 ? __uint_as_float(raw << 16)
+                                          : __half2float(__ushort_as_half((unsigned short)raw));
     ScaleParts p;
     p.hi = __float2bfloat162_rn(s);
     p.lo = __float2bfloat162_rn(s - __low2float(p.hi));
@@ -144,9 +159,11 @@ __device__ __forceinline__ ScaleParts split_scale(uint32_t raw, int stype) {
 }
 
 // Eight codes times a scale: four words of bf16 pairs in column order.
-// kLow: the scale has a low part.
-template <bool kLow>
-__device__ __forceinline__ void dequant8(uint32_t w, const ScaleParts& s, uint32_t* o) {
+// kLow: the scale has a low part.  kRest: to r what o lacks, c s_hi - o exactly
+// (a multiple of s_hi's last place, at most six of them), then + c s_lo rounded
+// to bf16: o + r is within 2^-16 of the weight.
+template <bool kLow, bool kRest>
+__device__ __forceinline__ void dequant8(uint32_t w, const ScaleParts& s, uint32_t* o, uint32_t* r) {
     const uint32_t w4 = w >> 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -156,6 +173,10 @@ __device__ __forceinline__ void dequant8(uint32_t w, const ScaleParts& s, uint32
                                          __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)));
         const __nv_bfloat162 h = kLow ? __hfma2(v, s.hi, __hmul2(v, s.lo)) : __hmul2(v, s.hi);
         o[j] = *reinterpret_cast<const uint32_t*>(&h);
+        if (kRest) {
+            const __nv_bfloat162 l = __hfma2(v, s.lo, __hfma2(v, s.hi, __hneg2(h)));
+            r[j] = *reinterpret_cast<const uint32_t*>(&l);
+        }
     }
 }
 
@@ -180,12 +201,14 @@ struct GemmPlan {
     int row_tiles;
 };
 
-template <int kN, bool kLow>
+template <int kN, bool kLow, bool kRest>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LinearArgs a,
                        GemmPlan p) {
     namespace cg = cooperative_groups;
-    using G = Geo<kN>;
+    using G = Geo<kN, kRest>;
+    constexpr int kACols = G::kACols;
+    static_assert(kLow || !kRest, "the rest is taken with both parts of the scale");
     extern __shared__ __align__(128) uint8_t dsm[];
     __shared__ uint64_t w_full[G::kWStages], w_empty[G::kWStages], x_full[G::kStages], a_full[G::kStages], empty[G::kStages], done_bar;
     __shared__ uint32_t tmem_slot;
@@ -283,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint64_t b = b0 + ((kb * (G::kXBytes / 2) + kk * 32) >> 4);
                         mma_ts(tmem, acol + kb * 32 + kk * 8, b, idesc, (i | kb | kk) != 0);
+                        if (kRest) mma_ts(tmem, acol + 64 + kb * 32 + kk * 8, b, idesc, 1);
                     }
                 commit(empty + t.s);
             }
@@ -339,16 +363,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_after();
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
-                uint32_t o[32];
+                auto codes = [&](int u) {  // 16-byte chunk 2 half + u of the row's 64 bytes (64-byte swizzle)
+                    return lds128(wrow + sw * kWBytes + (((2 * (half0 + h) + u) ^ ((r >> 1) & 3)) << 4));
+                };
+                if constexpr (kRest) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {  // 16-byte chunk 2 half + u of the row's 64 bytes (64-byte swizzle)
-                    const uint4 v = lds128(wrow + sw * kWBytes + (((2 * (half0 + h) + u) ^ ((r >> 1) & 3)) << 4));
-                    dequant8<kLow>(v.x, sp[h][u], o + 16 * u);
-                    dequant8<kLow>(v.y, sp[h][u], o + 16 * u + 4);
-                    dequant8<kLow>(v.z, sp[h][u], o + 16 * u + 8);
-                    dequant8<kLow>(v.w, sp[h][u], o + 16 * u + 12);
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t o[16], l[16];
+                        const uint4 v = codes(u);
+                        dequant8<kLow, true>(v.x, sp[h][u], o, l);
+                        dequant8<kLow, true>(v.y, sp[h][u], o + 4, l + 4);
+                        dequant8<kLow, true>(v.z, sp[h][u], o + 8, l + 8);
+                        dequant8<kLow, true>(v.w, sp[h][u], o + 12, l + 12);
+                        st_tmem16(at + s * kACols + h * 32 + 16 * u, o);
+                        st_tmem16(at + s * kACols + 64 + h * 32 + 16 * u, l);
+                    }
+                } else {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint4 v = codes(u);
+                        dequant8<kLow, false>(v.x, sp[h][u], o + 16 * u, nullptr);
+                        dequant8<kLow, false>(v.y, sp[h][u], o + 16 * u + 4, nullptr);
+                        dequant8<kLow, false>(v.z, sp[h][u], o + 16 * u + 8, nullptr);
+                        dequant8<kLow, false>(v.w, sp[h][u], o + 16 * u + 12, nullptr);
+                    }
+                    st_tmem32(at + s * kACols + h * 32, o);
                 }
-                st_tmem32(at + s * kACols + h * 32, o);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before();
@@ -480,10 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (size > 1) cluster.sync();  // no CTA is gone while another reads its tile
 }
 
-template <int kN, bool kLow>
+template <int kN, bool kLow, bool kRest>
 cudaError_t launch(const LinearArgs& a, int dev, int size, cudaStream_t stream) {
-    auto* k = linear_gemm_kernel<kN, kLow>;
-    using G = Geo<kN>;
+    auto* k = linear_gemm_kernel<kN, kLow, kRest>;
+    using G = Geo<kN, kRest>;
     static std::atomic<int> set[64];
     if (!set[dev]) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
@@ -524,14 +565,14 @@ cudaError_t capacity(int dev, const Capacity** out) {
     Capacity& cap = caps[dev];
     *out = &cap;
     if (cap.ctas[1] > 0) return cudaSuccess;
-    auto* k = linear_gemm_kernel<256, true>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<256>::kSmem);
+    auto* k = linear_gemm_kernel<256, true, false>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<256, false>::kSmem);
     for (int s = 8; s >= 1 && e == cudaSuccess; --s) {
         int n = 0;
         cudaLaunchConfig_t c = {};
         c.gridDim = dim3(s);
         c.blockDim = dim3(kThreads);
-        c.dynamicSmemBytes = Geo<256>::kSmem;
+        c.dynamicSmemBytes = Geo<256, false>::kSmem;
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeClusterDimension;
         at.val.clusterDim.x = s;
@@ -548,12 +589,34 @@ cudaError_t capacity(int dev, const Capacity** out) {
 // cluster's exchange, and what a launch takes that leaves the next one less
 // than half of the SMs to start on while it runs.  Fitted (8 % r.m.s.) to 1330
 // measured launches of 11 shapes from 256 x 1024 to 12288 x 2048, 20 to 512
-// tokens, each tile width and cluster size, one after another on a stream.
+// tokens, each tile width and cluster size, one after another on a stream.  With
+// weights in two parts a stage takes 1.7 times as long (1141 launches), and the
+// same costs choose within 2 % of the best on average, 33 % at worst.
 struct TileCost {
     int tokens, stage, fixed;
 };
 constexpr TileCost kTiles[] = {{16, 36, 160}, {32, 36, 184}, {64, 36, 257}, {128, 39, 379}, {256, 56, 648}};
 constexpr int kExchange = 53, kExchangeCta = 29, kCrowd = 200;
+
+template <bool kLow>
+cudaError_t launch_rounded(const LinearArgs& a, int tokens, int dev, int size, cudaStream_t stream) {
+    switch (tokens) {
+        case 16: return launch<16, kLow, false>(a, dev, size, stream);
+        case 32: return launch<32, kLow, false>(a, dev, size, stream);
+        case 64: return launch<64, kLow, false>(a, dev, size, stream);
+        case 128: return launch<128, kLow, false>(a, dev, size, stream);
+        default: return launch<256, kLow, false>(a, dev, size, stream);
+    }
+}
+
+cudaError_t launch_rest(const LinearArgs& a, int tokens, int dev, int size, cudaStream_t stream) {
+    switch (tokens) {
+        case 16: return launch<16, true, true>(a, dev, size, stream);
+        case 32: return launch<32, true, true>(a, dev, size, stream);
+        case 64: return launch<64, true, true>(a, dev, size, stream);
+        default: return launch<128, true, true>(a, dev, size, stream);
+    }
+}
 
 }  // namespace
 
@@ -571,10 +634,11 @@ cudaError_t launch_linear_gemm(const LinearArgs& a, cudaStream_t stream) {
     const Capacity* cap;
     if ((e = capacity(dev, &cap)) != cudaSuccess) return e;
     const int stages = (a.K + kStageK - 1) / kStageK;
+    const bool rest = a.full || a.T <= kStreamTok;
     int tokens = 0, size = 1;
     long long best = 0;
     for (const TileCost& c : kTiles) {
-        if (c.tokens >= 2 * a.T && c.tokens > 16) break;
+        if ((c.tokens >= 2 * a.T && c.tokens > 16) || (rest && c.tokens > 128)) break;
         const long long tiles = (long long)((a.N + kRows - 1) / kRows) * ((a.T + c.tokens - 1) / c.tokens);
         for (int s = 1; s <= 8 && s <= stages; ++s) {
             if (cap->ctas[s] == 0) continue;
@@ -588,14 +652,9 @@ cudaError_t launch_linear_gemm(const LinearArgs& a, cudaStream_t stream) {
             }
         }
     }
-    const bool low = a.stype != kScaleBf16;
-    switch (tokens) {
-        case 16: return low ? launch<16, true>(a, dev, size, stream) : launch<16, false>(a, dev, size, stream);
-        case 32: return low ? launch<32, true>(a, dev, size, stream) : launch<32, false>(a, dev, size, stream);
-        case 64: return low ? launch<64, true>(a, dev, size, stream) : launch<64, false>(a, dev, size, stream);
-        case 128: return low ? launch<128, true>(a, dev, size, stream) : launch<128, false>(a, dev, size, stream);
-        default: return low ? launch<256, true>(a, dev, size, stream) : launch<256, false>(a, dev, size, stream);
-    }
+    if (rest) return launch_rest(a, tokens, dev, size, stream);
+    return a.stype == kScaleBf16 ? launch_rounded<false>(a, tokens, dev, size, stream)
+                                 : launch_rounded<true>(a, tokens, dev, size, stream);
 }
 
 }  // namespace moe
