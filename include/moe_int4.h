@@ -402,8 +402,9 @@ int32_t moe_layer_path(const moe_cfg_t* cfg, int32_t T);
  * memory: T * (K rounded up to 256, + 64) to 57856) multiplies the codes with x
  * rounded to 16 bits, two int8 parts and a power-of-two scale: off by at most
  * 2^-15 of the largest magnitude of the 256 columns (k / 256) it is in, exact
- * integer sums within a scale group.  256 columns whose magnitudes are all
- * below 2^-113 count as zero; a token with a NaN or an infinity gets NaN in
+ * integer sums within a scale group.  256 columns (32 of h in
+ * moe_few_forward) whose magnitudes are all below 2^-113 are held to within
+ * 2^-128; a token with a NaN or an infinity gets NaN in
  * every output.  The other calls of moe_linear_forward run on the bf16 tensor
  * cores with x as it is.  Up to eight tokens, and with MOE_FULL_WEIGHTS any
  * number, they take each weight c * scale in two bf16 parts, off by at most

@@ -47,8 +47,9 @@ __device__ __forceinline__ int x_pos(int i) {
 }
 
 // Scale of 256 values whose largest magnitude has the bf16 bits m (sign
-// cleared): *s = 2^e with |v| / 2^e <= 127, *inv = 256 / s.  Magnitudes below
-// 2^-113 (e clamped at -119) become zero; NaN for NaN and infinity.
+// cleared): *s = 2^e with |v| / 2^e <= 127, *inv = 256 / s.  Below 2^-113 e stays
+// at -119 (256 / s is finite then) and a step is 2^-127, whatever the largest
+// magnitude; NaN for NaN and infinity.
 __device__ __forceinline__ void block_scale(uint32_t m, float* s, float* inv) {
     // |v| / 2^e in [64, 127]: the largest significand, 127.5 / 64, takes the next e
     const int e = max((int)(m >> 7) - 133 + ((m & 127) == 127), -119);

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests._group_int4 import codes, gen, linear64, linear_bound, linear_rms, scales
+from tests._group_int4 import block_max, codes, gen, linear64, linear_bound, linear_rms, scales, weights64
 
 pytestmark = pytest.mark.gpu
 
@@ -287,3 +287,34 @@ def test_wide_stores(moe, cuda_device, T, N):
             check(out, x, w, s, group, a)
             assert bool((buf[at:at + T * wide].view(T, wide)[:, N:] == 7).all())
             assert bool((buf[:at] == 7).all()) and bool((buf[at + T * wide:] == 7).all())
+
+
+@pytest.mark.parametrize("stype,group", [("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("T", [1, 4, 8, 24])
+def test_smallest_activations(moe, cuda_device, T, stype, group):
+    """Blocks of 256 columns around 2^-113, below which activations are held to 2^-128 and no longer to 2^-15 of the
+    block's largest; the scales bring the sums back into f32's normal range."""
+    N, K = 96, 1536
+    x, w, s, _ = make(T, N, K, group, stype, 41, False, cuda_device)
+    s *= 2.0 ** 80
+    g = gen(42, cuda_device)
+    for b, e in enumerate((-112, -113, -114, -120, -126, -130)):  # magnitudes in [2^(e-1), 2^e)
+        m = torch.randint(128, 256, (T, 256), generator=g, device=cuda_device).double() * 2.0 ** (e - 8)
+        m *= torch.randint(0, 2, (T, 256), generator=g, device=cuda_device) * 2 - 1
+        x[:, 256 * b:256 * (b + 1)] = m.to(torch.bfloat16)
+    assert float(x[:, -256:].abs().max()) <= 2.0 ** -130 and float(x[:, -256:].abs().min()) > 0
+    out = moe.linear_forward(x, w, s, group, flags=moe.MOE_OUT_F32)
+    W = weights64(w, s, group).abs()
+    mag = x.double().abs() @ W.t()
+    held = (2.0 ** -15 * block_max(x, 256)).clamp(min=2.0 ** -128)
+    b = held @ W.t() + (K / 16 + 64) * 2.0 ** -23 * mag
+    if T > 8:  # x as it is, subnormal values among it; each weight rounded to bf16
+        b = (2.0 ** -8 + 2.0 ** -16) * mag + (K / 16 + 64) * 2.0 ** -23 * mag
+    off = (out.double() - linear64(x, w, s, group)).abs()
+    assert bool((off <= b).all()), float((off / b).max())
+    # a block below 2^-113 counts: alone, it gives more than its bound
+    alone = x.clone()
+    alone[:, :512], alone[:, 768:] = 0, 0
+    want = linear64(alone, w, s, group)
+    got = moe.linear_forward(alone, w, s, group, flags=moe.MOE_OUT_F32).double()
+    assert float((got - want).norm() / want.norm()) <= (2.0 ** -12 if T <= 8 else 2.0 ** -8)
