@@ -424,7 +424,9 @@ int32_t moe_layer_path(const moe_cfg_t* cfg, int32_t T);
  *   K           : input features, a multiple of 32, 32..32768
  *   group       : columns per scale (see above)
  *   scale_type  : MOE_SCALE_*
- *   flags       : MOE_OUT_F32 (out is f32), MOE_FULL_WEIGHTS (see above)
+ *   flags       : MOE_OUT_F32 (out is f32), MOE_FULL_WEIGHTS (see above),
+ *                 MOE_TEST_STALL (test only: where the tensor cores run, the
+ *                 first block of the launch gives up after ~1 ms)
  *   ldx         : elements between rows of x (0: K); a multiple of 8, >= K
  *   ldo, lda    : elements between rows of out and of add (0: N), >= N */
 typedef struct moe_linear_cfg {
@@ -443,8 +445,9 @@ typedef struct moe_linear_cfg {
  * scales, and may overlap add only as the same bf16 tensor (same pointer and
  * stride: an in-place update).  A tensor reaches from its first to its last
  * element: two whose rows lie between one another's count as overlapping.  No
- * workspace; any number of calls may run at once.  A call whose waits on the
- * device give up (they are bounded; never in a correct run) leaves NaN. */
+ * workspace; any number of calls may run at once.  Waits on the device are
+ * bounded (about 2 s); a block whose wait gives up, which never happens in a
+ * correct run, leaves NaN in its 128 rows' outputs of its tokens. */
 int moe_linear_forward(const void* x, const uint8_t* w, const void* scales, const void* add, void* out, int32_t T,
                        const moe_linear_cfg_t* cfg, void* stream);
 

@@ -43,7 +43,7 @@ Range range(const void* p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + 
 int linear_args(const moe_linear_cfg_t* c, int32_t T, LinearArgs* a) {
     if (!c || c->struct_size != sizeof(moe_linear_cfg_t)) return MOE_ERR_INVALID_ARG;
     if (T < 0 || T > kMaxTokens || c->N <= 0 || c->K <= 0) return MOE_ERR_INVALID_ARG;
-    if (c->flags & ~(MOE_OUT_F32 | MOE_FULL_WEIGHTS)) return MOE_ERR_INVALID_ARG;
+    if (c->flags & ~(MOE_OUT_F32 | MOE_FULL_WEIGHTS | MOE_TEST_STALL)) return MOE_ERR_INVALID_ARG;
     if (c->scale_type < kScaleF32 || c->scale_type > kScaleF16) return MOE_ERR_INVALID_ARG;
     memset(a, 0, sizeof *a);
     a->T = T;
@@ -52,6 +52,7 @@ int linear_args(const moe_linear_cfg_t* c, int32_t T, LinearArgs* a) {
     a->stype = c->scale_type;
     a->out_f32 = (c->flags & MOE_OUT_F32) != 0;
     a->full = (c->flags & MOE_FULL_WEIGHTS) != 0;
+    a->stall = (c->flags & MOE_TEST_STALL) != 0;
     a->ldx = c->ldx ? c->ldx : c->K;
     a->ldo = c->ldo ? c->ldo : c->N;
     a->lda = c->lda ? c->lda : c->N;

@@ -27,7 +27,8 @@ struct LinearArgs {
     int T, N, K;
     int gshift, G;  // columns per scale: 1 << gshift; scales per row
     int stype, out_f32;
-    int full;  // MOE_FULL_WEIGHTS
+    int full;   // MOE_FULL_WEIGHTS
+    int stall;  // MOE_TEST_STALL
     long long ldx, ldo, lda;
 };
 

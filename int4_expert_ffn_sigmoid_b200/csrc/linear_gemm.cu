@@ -27,7 +27,8 @@
 // Roles (864 threads, one CTA per SM): warps 0-23 convert (in groups that take
 // the stages in turn) and then read the accumulators out; warps 24 and 25
 // issue the TMA loads of the codes and of x, warp 26 the MMAs.  Every wait is
-// bounded; a CTA whose wait gave up (never, in a correct run) stores NaN.
+// bounded; a CTA whose wait gave up (never, in a correct run) stores NaN.  Under
+// MOE_TEST_STALL the first CTA's codes stop half way.
 //
 // What bounds it.  64 tokens x 6144 x 6144: 13.9 us (3.4 at the copy rate): the
 // MMAs' pace over the stages of one CTA, 96 of the 148 SMs (48 row tiles in
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(128) uint8_t dsm[];
     __shared__ uint64_t w_full[G::kWStages], w_empty[G::kWStages], x_full[G::kStages], a_full[G::kStages], empty[G::kStages], done_bar;
     __shared__ uint32_t tmem_slot;
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_never;
     volatile int* abort = &s_abort;
     // warp-uniform to the compiler too: the MMA warp's descriptors then live in uniform registers
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(empty + i, 1);  // the MMAs' commit
         }
         bar_init(&done_bar, 1);
-        s_abort = 0;
+        s_abort = s_never = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kWarpMma) {
@@ -254,8 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpW) {
         const bool leader = elect_one();
         Slot<G::kWStages> w;
+        const int upto = a.stall && blockIdx.x == 0 ? n / 2 : n;
         int i = 0;
-        for (int x = st0 * (kStageK / 2); i < n; ++i, x += kStageK / 2) {  // weights do not depend on the kernel before this one
+        for (int x = st0 * (kStageK / 2); i < upto; ++i, x += kStageK / 2) {  // weights do not depend on the kernel before this one
             if (i >= G::kWStages && !warp_wait(w_empty + w.s, w.ph ^ 1u, abort)) break;
             if (leader) {
                 refill_fence();
@@ -263,6 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_tile(wring + w.s * kWBytes, &map_w, w_full + w.s, x, row0);
             }
             w.step();
+        }
+        if (upto < n) {  // every other role waits for the rest
+            stall_on_unset_flag(&s_never, kStallCycles);
+            *abort = 1;
         }
         // every copy lands before the CTA's shared memory is reused or goes away
         for (int j = i > G::kWStages ? i - G::kWStages : 0; j < i; ++j)

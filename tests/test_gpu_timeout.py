@@ -137,3 +137,35 @@ def test_fused_stack_bad_index_and_poison(moe, cuda_device):
     poisoned = moe.stack_forward(x, stacked, shape, workspace=ws, flags=f | moe.MOE_DEBUG_POISON)
     torch.cuda.synchronize()
     assert torch.equal(poisoned, good)
+
+
+# --- the projection's tensor-core kernel: no status word, NaN instead --------------
+
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("T,N,K,what", [(40, 200 * 128, 1024, "one block a tile"), (16, 256, 8192, "a cluster a tile"),
+                                        (300, 40 * 128, 2048, "wide tiles"), (9, 128, 128, "one stage")])
+def test_linear_gives_up_and_recovers(moe, cuda_device, T, N, K, what, full):
+    """The first block's loading warp stops half way, waits ~1 ms on a flag that nothing sets and gives up, while the
+    converters, the MMA warp and the loads of x wait for the rest and have to give up too.  Its tile is NaN, a cluster's whole tile too; every other output and the next call are as ever."""
+    from tests._group_int4 import codes, gen, scales
+    g = gen(T, cuda_device)
+    x = torch.randn((T, K), generator=g, device=cuda_device).to(torch.bfloat16)
+    lin = moe.Int4Linear(codes(g, N, K // 2), scales(g, (N,), K, 64, "bf16"), 64)
+    f = moe.MOE_FULL_WEIGHTS if full else 0
+    good = lin(x, flags=f)
+    bad = lin(x, flags=f | moe.MOE_TEST_STALL)
+    again = lin(x, flags=f)
+    torch.cuda.synchronize()
+    assert torch.equal(again, good), what
+    nan = torch.isnan(bad)
+    rows, toks = int(nan.any(0).sum()), int(nan.any(1).sum())
+    assert bool(nan[:toks, :rows].all()) and rows == 128 and 0 < toks <= T and int(nan.sum()) == rows * toks, what
+    assert torch.equal(bad[~nan], good[~nan]), what
+
+
+def test_streaming_linear_has_no_waits_to_give_up(moe, cuda_device):
+    from tests._group_int4 import codes, gen, scales
+    g = gen(4, cuda_device)
+    x = torch.randn((4, 1024), generator=g, device=cuda_device).to(torch.bfloat16)
+    lin = moe.Int4Linear(codes(g, 256, 512), scales(g, (256,), 1024, 64, "bf16"), 64)
+    assert torch.equal(lin(x, flags=moe.MOE_TEST_STALL), lin(x))
