@@ -33,6 +33,14 @@
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Calls are
  *    stream-ordered and asynchronous: the return value reports argument
  *    errors and launch errors only, unless MOE_DEBUG_CHECK is set.
+ *  - A call may start while the kernel ahead of it in the stream finishes, and
+ *    reads constants (codes, scales, router weights and bias) before it waits
+ *    for that kernel; x, add, out and the workspace are touched after the wait.
+ *    So the kernel directly ahead may write a call's constants only if it does
+ *    not let its dependents start early (griddepcontrol.launch_dependents /
+ *    cudaTriggerProgrammaticLaunchCompletion).  Copies, memsets and PyTorch's
+ *    kernels do not; this library's kernels do, so an output of one call is not
+ *    a constant of the next.
  *  - Calls are reentrant provided concurrent calls use distinct workspaces
  *    and outputs.  `out` must not alias `x`.
  */

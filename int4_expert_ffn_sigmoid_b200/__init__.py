@@ -488,7 +488,8 @@ class Int4Linear:
 
     ``w``: uint8 [N, K/2] packed codes; ``scales``: float32, bfloat16 or float16 [N, ceil(K/group)]
     ([N] with ``group`` = 0, one scale a row).  Calls may run at the same time, on any stream of the
-    weights' device."""
+    weights' device.  Weights are read before the kernel ahead on the stream has ended: PyTorch operations may
+    write them there, kernels that start their dependents early (this library's among them) may not."""
 
     def __init__(self, w: torch.Tensor, scales: torch.Tensor, group: int = 128):
         if w.dim() != 2:
@@ -602,7 +603,8 @@ class MoEFewLayer:
     ``layer_forward`` but with scales [..., rows, ceil(cols/group)] of one type (float32, bfloat16 or float16);
     ``group`` = 0 takes ``layer_forward``'s own scales [..., rows].  Holds a workspace for calls of up to
     ``max_tokens`` tokens: its calls are ordered on one stream; give each stream that may run at the same time (each
-    captured graph among them) a ``workspace`` of its own (``new_workspace``)."""
+    captured graph among them) a ``workspace`` of its own (``new_workspace``).  What ``Int4Linear`` says of its
+    weights holds for the layer's too."""
 
     def __init__(self, layer: dict, shape, group: int = 0, max_tokens: int = 8, topp: float = 0.0):
         H, E, I, Is = shape.H, shape.E, shape.I, shape.Is

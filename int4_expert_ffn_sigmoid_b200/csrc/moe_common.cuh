@@ -137,7 +137,9 @@ struct Ctrl {
 // Programmatic dependent launch: every kernel of a call is launched so that
 // it may start while its predecessor in the stream finishes.  pdl_wait()
 // blocks until the predecessor grid has completed and its writes are
-// visible; nothing produced by an earlier kernel is touched before it.
+// visible.  Before it a kernel touches nothing that an earlier kernel of the
+// library produced, nor x, add, out or the workspace; codes, scales and router
+// constants it may read (the C ABI's conventions say what that asks of callers).
 // pdl_release() lets the next kernel launch (it still waits for this grid's
 // completion before reading anything).  Both are no-ops when the kernel was
 // launched without the attribute.
