@@ -23,7 +23,7 @@
 // kernels are held by their instructions (59 and 67 % of the issue slots at
 // five tokens, 49 and 33 % of DRAM's peak): about 300 a warp for 16 rows x 256
 // columns of the down kernel, of whose time the mma products take 14 % and the
-// loads of h 7 %.  64 experts of 1024 x 512, 2 picked, one token: 10.0 us against
+// loads of h 7 %.  64 experts of 1024 x 512, 2 picked, one token: 10.1 us against
 // 0.95, none of it bandwidth: the chain logits - exchange - selection (1.0) - first
 // routed weights from HBM (1.4) - down (2.4), and two launches.
 #include <cooperative_groups.h>
@@ -47,7 +47,8 @@ constexpr int kFewXMax = 98 * 1024;
 // CTAs that share the router: a cluster of kFewCluster computes all logits,
 // each CTA those of an eighth of the experts, and exchanges them in shared
 // memory.  Clusters of eight leave 120 of 148 SMs usable, of four 132, of two
-// all (64 experts of 1024 x 512, one token: 9.4, 9.8 and 10.8 us).  With router
+// all (64 experts of 1024 x 512, one, four and eight tokens: 10.1, 11.5 and 16.7;
+// 10.5, 11.9 and 17.4; 11.3, 13.2 and 19.5 us).  With router
 // weights beyond kFewRouterMax, or gate and up weights beyond kFewWeightsMax
 // (elements of h times H), the logits are a kernel of their own in front
 // (router_logits_kernel) and every SM takes part in this one.  Logits here and

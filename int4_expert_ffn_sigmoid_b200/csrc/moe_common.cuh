@@ -138,8 +138,9 @@ struct Ctrl {
 // it may start while its predecessor in the stream finishes.  pdl_wait()
 // blocks until the predecessor grid has completed and its writes are
 // visible.  Before it a kernel touches nothing that an earlier kernel of the
-// library produced, nor x, add, out or the workspace; codes, scales and router
-// constants it may read (the C ABI's conventions say what that asks of callers).
+// library produced, nor x, add, out or the workspace (but see few_gate_up_kernel
+// for x); codes, scales and router constants it may read (the C ABI's
+// conventions say what that asks of callers).
 // pdl_release() lets the next kernel launch (it still waits for this grid's
 // completion before reading anything).  Both are no-ops when the kernel was
 // launched without the attribute.
