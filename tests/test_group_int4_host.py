@@ -162,3 +162,16 @@ def test_few_refuses_overlaps(moe):
     assert call(out=out, idx=out + 8 * 256 * 2 - 16) == INV and call(out=out, flags=moe.MOE_OUT_F32, w=out + 8 * 256 * 2) == INV
     assert call(out=out, idx=3 << 20, w=3 << 20) == INV and call(out=out, ws=4 << 20) == INV and call(out=out, idx=4 << 20) == INV
     assert call(out=4 << 20, T=0) == 0  # nothing is read or written
+
+
+def test_full_weights_flag(moe):
+    import re
+    with open(HEADER) as f:
+        bit = re.search(r"#define MOE_FULL_WEIGHTS \(1u << (\d+)\)", f.read())
+    assert moe.MOE_FULL_WEIGHTS == 1 << int(bit.group(1))
+    f = moe.MOE_FULL_WEIGHTS
+    for flags in (f, f | moe.MOE_OUT_F32, moe.MOE_TEST_STALL, f | moe.MOE_TEST_STALL):
+        assert linear(moe, flags=flags) == 0  # T = 0: nothing to do
+    assert linear(moe, flags=f | moe.MOE_ADD_RESIDUAL) == moe.MOE_ERR_INVALID_ARG
+    assert few(moe, flags=f) == moe.MOE_ERR_INVALID_ARG  # always streams
+    assert few(moe, flags=moe.MOE_TEST_STALL) == moe.MOE_ERR_INVALID_ARG
