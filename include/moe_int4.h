@@ -415,8 +415,8 @@ int32_t moe_layer_path(const moe_cfg_t* cfg, int32_t T);
  * 2^-128; a token with a NaN or an infinity gets NaN in
  * every output.  The other calls of moe_linear_forward run on the bf16 tensor
  * cores with x as it is.  Up to eight tokens, and with MOE_FULL_WEIGHTS any
- * number, they take each weight c * scale in two bf16 parts, off by at most
- * 2^-16 of it: one accuracy for one token and for eight.  More tokens take it
+ * number, they take each weight c * scale in two bf16 parts, off by less than
+ * 2^-15 of it: one accuracy for one token and for eight.  More tokens take it
  * in one part, rounded once to bf16 (off by up to 2^-8 of it): beside a bf16
  * output's own rounding (relative L2 error 1.7e-3) the result is then off by
  * 2.0e-3 to 2.4e-3, and under MOE_OUT_F32 by 1.2e-3 to 1.7e-3 where the full

@@ -12,7 +12,7 @@
 // Two forms.  One part: each weight is rounded once to bf16 (2^-8 of it at
 // most; the codes 0, 1, 2, 4 and 8 times a bf16 scale are exact).  Two parts
 // (kRest): what that rounding left is a second bf16 matrix and each step takes
-// a second MMA, which holds a weight to 2^-16.  Two parts are taken for up to
+// a second MMA, which holds a weight to 2^-15.  Two parts are taken for up to
 // eight tokens, where weight streaming is as good and a token's accuracy should
 // not hang on its company, and under MOE_FULL_WEIGHTS.  They cost 64 tokens x
 // 6144 x 6144 13.5 -> 19.7 us, 512 x 4096 x 6144 22.6 -> 38.7, 16 x 6144 x 2048 6.3
@@ -161,8 +161,9 @@ __device__ __forceinline__ ScaleParts split_scale(uint32_t raw, int stype) {
 
 // Eight codes times a scale: four words of bf16 pairs in column order.
 // kLow: the scale has a low part.  kRest: to r what o lacks, c s_hi - o exactly
-// (a multiple of s_hi's last place, at most six of them), then + c s_lo rounded
-// to bf16: o + r is within 2^-16 of the weight.
+// (a multiple of s_hi's last place, at most eight of them), then + c s_lo rounded
+// to bf16.  The scale's two parts and r's rounding are off by 2^-16 of the weight
+// at most each (together by 1.03 times that over two million scales and all codes).
 template <bool kLow, bool kRest>
 __device__ __forceinline__ void dequant8(uint32_t w, const ScaleParts& s, uint32_t* o, uint32_t* r) {
     const uint32_t w4 = w >> 4;

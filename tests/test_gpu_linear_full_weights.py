@@ -15,12 +15,13 @@ def moe():
 
 
 def bound(x, w, s, group, add=None, streamed=False):
-    """A weight's two bf16 parts hold it to 2^-16; weight streaming holds an activation to 2^-15 of the largest of its
+    """A weight's two bf16 parts hold it to 2^-15: the scale's second part is off by half a step (2^-8) of at most 2^-8 of
+    the scale, and so is the weight's; weight streaming holds an activation to 2^-15 of the largest of its
     256 columns, which is more.  Sums: as in linear_bound, an f32 chain of at most K / 16 + 64 additions, two products
     a weight here: K / 8 + 64."""
     W = weights64(w, s, group).abs()
     mag = x.double().abs() @ W.t()
-    b = 2.0 ** -15 * (block_max(x, 256) @ W.t()) if streamed else 2.0 ** -16 * mag
+    b = 2.0 ** -15 * (block_max(x, 256) @ W.t()) if streamed else 2.0 ** -15 * mag
     b = b + (x.shape[1] / 8 + 64) * 2.0 ** -23 * mag
     return b if add is None else b + 2.0 ** -23 * (mag + add.double().abs())
 
@@ -34,7 +35,7 @@ def check(out, x, w, s, group, add=None, streamed=False):
     want, b = linear64(x, w, s, group, add), bound(x, w, s, group, add, streamed)
     off = (out.double() - want).abs()
     assert bool((off <= b).all()), float((off / b).max())
-    # independent errors of at most 2^-15 of a block's largest (under 2^-13 of its r.m.s.), or of 2^-16 of a weight
+    # independent errors of at most 2^-15 of a block's largest (under 2^-13 of its r.m.s.), or of 2^-15 of a weight
     assert float((out.double() - want).norm() / want.norm()) <= 2.0 ** -12
 
 
